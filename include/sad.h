@@ -500,6 +500,131 @@ const char *sad_last_error(const sad_ctx *ctx);
 int sad_backward_noalloc(int H, int W, int N_cap, const float *records, const uint32_t *table,
                          const float *target, float *image, float *grads, double *loss, sad_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Feature fields: D channels per site beside its colour
+ *
+ * A site may carry a row of D values (class scores, an embedding).  A pixel's
+ * row is the blend of its K candidate sites' rows with the softmax weights of
+ * the render, which is what a mixture of experts does with tokens: pixels are
+ * the rows (tokens), sites the experts and a pixel's candidate list the
+ * router's choice.  The calls below route rows to their experts, take rows
+ * out and back with weights, normalise rows and learn them from a teacher,
+ * each with its gradient.  They need no context: every size is an argument.
+ *
+ * Conventions.  T = n_rows rows, K = 1 ... 8 slots per row (SAD_K at most),
+ * n = T K < 2^31 pairs; pair j = t K + k.  ids: int32 [T][K]; an id outside
+ * [0, n_sites) (SAD_EMPTY read as int32 is -1) is an empty slot.  weights,
+ * dweights: float32 [T][K]; weights at empty slots are not read, dweights
+ * there are 0.  Row matrices hold D elements of the given type (SAD_F32,
+ * SAD_BF16, SAD_F16) per row, consecutive, with ld elements from one row to
+ * the next (ld >= D); other arrays are dense.  Sums, dot products and
+ * statistics are float32; a result of a 16-bit type is rounded once, to
+ * nearest even.  No float atomics: results are the same bits on every run.
+ * All pointers are device memory of the current device, whose stream is
+ * given; row matrices are aligned to their element, workspaces to 16 bytes.
+ * Outputs must not overlap inputs except where said.  Every call is
+ * asynchronous, allocates nothing and may be captured into a graph;
+ * workspaces are scratch for the one call (calls that may overlap need one
+ * each) and need no initialisation.  n_rows = 0 is valid.
+ * Errors: SAD_ERR_INVALID_ARG (NULL, misaligned, ld < D, bad size),
+ * SAD_ERR_UNSUPPORTED (K > 8, unknown type, D or M beyond the stated bound),
+ * SAD_ERR_CAPACITY (n >= 2^31), SAD_ERR_CUDA; sad_feature_error() says more.
+ * ------------------------------------------------------------------------ */
+#define SAD_F32 0
+#define SAD_BF16 1
+#define SAD_F16 2
+
+/* Message of the calling thread's last failing feature call ("" if none). */
+const char *sad_feature_error(void);
+
+/* Candidate ids and blend weights of every pixel of the current table:
+ * ids int32 [P][8] (-1 where a slot takes no part: empty, beyond N_cap,
+ * inactive, or with a logit that is not finite) and weights
+ * float32 [P][8] (0 there), in slot order: the w of sad_render.  On a coarser
+ * candidate grid a pixel reads its cell's list.  Both 16-byte aligned. */
+int sad_blend_weights(sad_ctx *ctx, int32_t *ids, float *weights, sad_stream_t stream);
+
+/* Rows sorted by expert, stable: offsets int32 [n_sites + 1] with offsets[e]
+ * = number of pairs whose id is valid and below e; place int32 [T][K] = the
+ * pair's position, offsets[e] + (earlier pairs of the same e), or -1 for an
+ * empty slot; order int32 [n] with order[place[j]] = j, and -1 behind the
+ * last pair.  1 <= n_sites < 2^30. */
+int sad_route_workspace_bytes(int64_t n_rows, int K, int n_sites, size_t *bytes);
+int sad_route(const int32_t *ids, int64_t n_rows, int K, int n_sites, int32_t *offsets, int32_t *order,
+              int32_t *place, void *workspace, size_t workspace_bytes, sad_stream_t stream);
+
+/* Rows out to their experts: xs[place[j]] = w_j x[t] (weights NULL: 1).  xs
+ * has n rows; those that no pair names (behind the last one) are left as
+ * they were.  Backward: dx[t] = sum_k w_j dxs[place[j]], dweights[j] =
+ * <dxs[place[j]], x[t]> (dweights NULL: not wanted, x may be NULL then). */
+int sad_dispatch(int dtype, const void *x, int64_t ldx, const float *weights, const int32_t *place, int64_t n_rows,
+                 int K, int D, void *xs, int64_t ldxs, sad_stream_t stream);
+int sad_dispatch_backward(int dtype, const void *dxs, int64_t lddxs, const void *x, int64_t ldx,
+                          const float *weights, const int32_t *place, int64_t n_rows, int K, int D, void *dx,
+                          int64_t lddx, float *dweights, sad_stream_t stream);
+
+/* Rows back from their experts: out[t] = sum_k w_j y[place[j]], k ascending
+ * (weights NULL: 1; a row without a pair gives 0).  Backward: dy[place[j]] =
+ * w_j dout[t] (rows that no pair names are left as they were), dweights[j] =
+ * <y[place[j]], dout[t]> (dweights NULL: not wanted, y may be NULL then). */
+int sad_combine(int dtype, const void *y, int64_t ldy, const float *weights, const int32_t *place, int64_t n_rows,
+                int K, int D, void *out, int64_t ldout, sad_stream_t stream);
+int sad_combine_backward(int dtype, const void *dout, int64_t lddout, const void *y, int64_t ldy,
+                         const float *weights, const int32_t *place, int64_t n_rows, int K, int D, void *dy,
+                         int64_t lddy, float *dweights, sad_stream_t stream);
+
+/* Rows that all pairs of a site share: out[t] = sum_k w_j F[e_j], F of
+ * n_sites rows; needs no routing.  Backward: dF[e] = sum of w_j dout[t] over
+ * the pairs j of e in order (float32 [n_sites][D], overwritten; 0 for a site
+ * without pairs), with offsets and order as sad_route gives them for these
+ * ids, and dweights[j] = <F[e_j], dout[t]>.  dF or dweights may be NULL (then
+ * offsets, order, workspace, or F, may be NULL too). */
+int sad_blend(int dtype, const void *F, int64_t ldf, int n_sites, const int32_t *ids, const float *weights,
+              int64_t n_rows, int K, int D, void *out, int64_t ldout, sad_stream_t stream);
+int sad_blend_workspace_bytes(int64_t n_rows, int K, int n_sites, int D, size_t *bytes);
+int sad_blend_backward(int dtype, const void *dout, int64_t lddout, const void *F, int64_t ldf, int n_sites,
+                       const int32_t *ids, const float *weights, const int32_t *offsets, const int32_t *order,
+                       int64_t n_rows, int K, int D, float *dF, float *dweights, void *workspace,
+                       size_t workspace_bytes, sad_stream_t stream);
+
+/* Layer norm of every row: mean and variance over its D values (the mean of
+ * squared deviations), rstd = 1 / sqrt(var + eps), y = (x - mean) rstd gamma
+ * + beta; gamma, beta float32 [D] (NULL: 1, 0); mean, rstd float32 [T] (NULL:
+ * not wanted).  Backward from dy, x and the saved mean and rstd: with g = dy
+ * gamma and h = (x - mean) rstd, dx = rstd (g - mean(g) - h mean(g h)),
+ * dgamma = sum over rows of dy h, dbeta = sum of dy (float32 [D], overwritten;
+ * both NULL: not wanted).  1 <= D <= 16384; y may be x, dx may be dy.
+ * eps >= 0. */
+#define SAD_NORM_MAX_D 16384
+int sad_layer_norm(int dtype, const void *x, int64_t ldx, const float *gamma, const float *beta, float eps,
+                   int64_t n_rows, int D, void *y, int64_t ldy, float *mean, float *rstd, sad_stream_t stream);
+int sad_layer_norm_workspace_bytes(int64_t n_rows, int D, size_t *bytes);
+int sad_layer_norm_backward(int dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, const float *gamma,
+                            const float *mean, const float *rstd, int64_t n_rows, int D, void *dx, int64_t lddx,
+                            float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
+                            sad_stream_t stream);
+
+/* Distillation from a teacher's top logits.  logits: T rows of V classes;
+ * teacher_ids int32 [T][M], teacher_logits float32 [T][M]: the teacher's M
+ * best classes of the row, in any order.  An entry counts when its id lies in
+ * [0, V) and its logit is not -infinity; the logits of other entries are not
+ * read.  With q = softmax of the row's counting teacher logits / tau and p =
+ * softmax(logits / tau),
+ *     loss[t] = rw_t tau^2 sum_m q_m (ln q_m - ln p[id_m]),
+ *     dlogits[t][v] = rw_t tau (p_v - sum of q_m over id_m = v),
+ * terms with q_m = 0 counting 0.  An id listed twice counts with both its q.
+ * row_weight float32 [T] (NULL: 1).  A row whose weight is 0, whose teacher
+ * entries all fail to count, or whose logits are all -infinity has loss 0
+ * and gradient 0, whatever else it holds (a teacher class that the student
+ * masks with -infinity in a row that keeps others gives an infinite loss and
+ * a finite gradient).  dlogits (the type of logits) NULL: loss only; it may
+ * be logits (same ld).  1 <= M <= 128, V < 2^30, 1e-30 <= tau <=
+ * 1e30. */
+#define SAD_DISTILL_MAX_M 128
+int sad_distill(int dtype, const void *logits, int64_t ld, const int32_t *teacher_ids, const float *teacher_logits,
+                const float *row_weight, int64_t n_rows, int V, int M, float tau, float *loss, void *dlogits,
+                int64_t lddlogits, sad_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,7 +3,8 @@
 The computation lives in ``libsad.so`` (CUDA kernels behind the C ABI of
 ``include/sad.h``).  ``_lib`` exposes every C entry point under its C name;
 ``Sad`` below owns the device buffers as PyTorch tensors (PyTorch is used for
-memory and streams only) and forwards each call to the library.
+memory and streams only) and forwards each call to the library.  ``features``
+holds the operators of feature fields (channels beside the colour).
 """
 from __future__ import annotations
 
@@ -217,6 +218,21 @@ class Sad:
     def render(self, image=None):
         _lib.sad_render(self.ctx, image, self.stream)
         return image if image is not None else self.image
+
+    def blend_weights(self, ids=None, weights=None):
+        """The render's softmax as rows: (ids (P, 8) int32, weights (P, 8)
+        float32), -1 and 0 where a slot takes no part.  With them a feature
+        field (``features``) is blended, routed and learned."""
+        t = self.torch
+        if ids is None:
+            ids = t.empty((self.P, 8), dtype=t.int32, device=self.device)
+        if weights is None:
+            weights = t.empty((self.P, 8), dtype=t.float32, device=self.device)
+        for x, d in ((ids, t.int32), (weights, t.float32)):
+            if x.shape != (self.P, 8) or x.dtype != d or not x.is_contiguous() or x.device != self.params.device:
+                raise SadError(_lib.SAD_ERR_INVALID_ARG, "ids and weights must be dense (P, 8) int32 and float32")
+        _lib.sad_blend_weights(self.ctx, ids, weights, self.stream)
+        return ids, weights
 
     def backward(self, flags: int = 0):
         _lib.sad_backward(self.ctx, flags, self.stream)

@@ -21,6 +21,11 @@ SAD_ERR_NOT_BOUND = 5
 SAD_K = 8
 SAD_MAX_INJECT = 64
 SAD_EMPTY = 0xFFFFFFFF
+SAD_F32 = 0
+SAD_BF16 = 1
+SAD_F16 = 2
+SAD_NORM_MAX_D = 16384
+SAD_DISTILL_MAX_M = 128
 
 _STATUS = {0: "SAD_OK", 1: "SAD_ERR_INVALID_ARG", 2: "SAD_ERR_UNSUPPORTED", 3: "SAD_ERR_CUDA",
            4: "SAD_ERR_CAPACITY", 5: "SAD_ERR_NOT_BOUND"}
@@ -86,6 +91,10 @@ EXPORTED = (
     "sad_render", "sad_backward", "sad_densify_prune", "sad_tau_diffuse", "sad_adam_step", "sad_fit_pass", "sad_fit_iteration", "sad_get_table", "sad_set_table",
     "sad_get_stats", "sad_get_loss", "sad_copy_loss", "sad_last_error", "sad_backward_noalloc",
     "sad_get_fit_state", "sad_set_fit_state", "sad_set_candidate_precision", "sad_set_list_staging",
+    "sad_feature_error", "sad_blend_weights", "sad_route_workspace_bytes", "sad_route", "sad_dispatch",
+    "sad_dispatch_backward", "sad_combine", "sad_combine_backward", "sad_blend", "sad_blend_workspace_bytes",
+    "sad_blend_backward", "sad_layer_norm", "sad_layer_norm_workspace_bytes", "sad_layer_norm_backward",
+    "sad_distill",
 )
 
 _lib = None
@@ -110,6 +119,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         raise ImportError(f"libsad is not built: {path} is missing")
     L = ctypes.CDLL(path)
     vp, ci, cu32, ci64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_int64
+    cf, csz = ctypes.c_float, ctypes.c_size_t
     sig = {
         "sad_workspace_bytes": [ci, ci, ci, ctypes.POINTER(ctypes.c_size_t)],
         "sad_create": [ci, ci, ci, ci, ctypes.POINTER(vp)],
@@ -148,11 +158,26 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "sad_set_fit_state": [vp, ctypes.POINTER(sad_fit_state), vp],
         "sad_set_candidate_precision": [vp, ci, vp],
         "sad_set_list_staging": [vp, ci, vp],
+        "sad_feature_error": [],
+        "sad_blend_weights": [vp, vp, vp, vp],
+        "sad_route_workspace_bytes": [ci64, ci, ci, ctypes.POINTER(ctypes.c_size_t)],
+        "sad_route": [vp, ci64, ci, ci, vp, vp, vp, vp, csz, vp],
+        "sad_dispatch": [ci, vp, ci64, vp, vp, ci64, ci, ci, vp, ci64, vp],
+        "sad_dispatch_backward": [ci, vp, ci64, vp, ci64, vp, vp, ci64, ci, ci, vp, ci64, vp, vp],
+        "sad_combine": [ci, vp, ci64, vp, vp, ci64, ci, ci, vp, ci64, vp],
+        "sad_combine_backward": [ci, vp, ci64, vp, ci64, vp, vp, ci64, ci, ci, vp, ci64, vp, vp],
+        "sad_blend": [ci, vp, ci64, ci, vp, vp, ci64, ci, ci, vp, ci64, vp],
+        "sad_blend_workspace_bytes": [ci64, ci, ci, ci, ctypes.POINTER(ctypes.c_size_t)],
+        "sad_blend_backward": [ci, vp, ci64, vp, ci64, ci, vp, vp, vp, vp, ci64, ci, ci, vp, vp, vp, csz, vp],
+        "sad_layer_norm": [ci, vp, ci64, vp, vp, cf, ci64, ci, vp, ci64, vp, vp, vp],
+        "sad_layer_norm_workspace_bytes": [ci64, ci, ctypes.POINTER(ctypes.c_size_t)],
+        "sad_layer_norm_backward": [ci, vp, ci64, vp, ci64, vp, vp, vp, ci64, ci, vp, ci64, vp, vp, vp, csz, vp],
+        "sad_distill": [ci, vp, ci64, vp, vp, vp, ci64, ci, ci, cf, vp, vp, ci64, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
         f.argtypes = args
-        f.restype = ctypes.c_char_p if name == "sad_last_error" else ci
+        f.restype = ctypes.c_char_p if name in ("sad_last_error", "sad_feature_error") else ci
     _lib = L
     return L
 
@@ -357,3 +382,100 @@ def sad_backward_noalloc(H: int, W: int, N_cap: int, records, table, target, ima
     that cannot allocate device memory (see include/sad.h)."""
     _check(None, load().sad_backward_noalloc(H, W, N_cap, _ptr(records), _ptr(table), _ptr(target), _ptr(image),
                                              _ptr(grads), _ptr(loss), _stream(stream)))
+
+
+# ---- feature fields (no context; messages come from sad_feature_error) -------
+
+def sad_feature_error() -> str:
+    return load().sad_feature_error().decode()
+
+
+def _check_feature(status: int) -> None:
+    if status != SAD_OK:
+        raise SadError(status, sad_feature_error())
+
+
+def sad_blend_weights(ctx: int, ids, weights, stream=None) -> None:
+    _check(ctx, load().sad_blend_weights(ctx, _ptr(ids), _ptr(weights), _stream(stream)))
+
+
+def sad_route_workspace_bytes(n_rows: int, K: int, n_sites: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check_feature(load().sad_route_workspace_bytes(n_rows, K, n_sites, ctypes.byref(out)))
+    return out.value
+
+
+def sad_route(ids, n_rows: int, K: int, n_sites: int, offsets, order, place, workspace, workspace_bytes: int,
+              stream=None) -> None:
+    _check_feature(load().sad_route(_ptr(ids), n_rows, K, n_sites, _ptr(offsets), _ptr(order), _ptr(place),
+                                    _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sad_dispatch(dtype: int, x, ldx: int, weights, place, n_rows: int, K: int, D: int, xs, ldxs: int,
+                 stream=None) -> None:
+    _check_feature(load().sad_dispatch(dtype, _ptr(x), ldx, _ptr(weights), _ptr(place), n_rows, K, D, _ptr(xs), ldxs,
+                                       _stream(stream)))
+
+
+def sad_dispatch_backward(dtype: int, dxs, lddxs: int, x, ldx: int, weights, place, n_rows: int, K: int, D: int, dx,
+                          lddx: int, dweights, stream=None) -> None:
+    _check_feature(load().sad_dispatch_backward(dtype, _ptr(dxs), lddxs, _ptr(x), ldx, _ptr(weights), _ptr(place),
+                                                n_rows, K, D, _ptr(dx), lddx, _ptr(dweights), _stream(stream)))
+
+
+def sad_combine(dtype: int, y, ldy: int, weights, place, n_rows: int, K: int, D: int, out, ldout: int,
+                stream=None) -> None:
+    _check_feature(load().sad_combine(dtype, _ptr(y), ldy, _ptr(weights), _ptr(place), n_rows, K, D, _ptr(out), ldout,
+                                      _stream(stream)))
+
+
+def sad_combine_backward(dtype: int, dout, lddout: int, y, ldy: int, weights, place, n_rows: int, K: int, D: int, dy,
+                         lddy: int, dweights, stream=None) -> None:
+    _check_feature(load().sad_combine_backward(dtype, _ptr(dout), lddout, _ptr(y), ldy, _ptr(weights), _ptr(place),
+                                               n_rows, K, D, _ptr(dy), lddy, _ptr(dweights), _stream(stream)))
+
+
+def sad_blend(dtype: int, F, ldf: int, n_sites: int, ids, weights, n_rows: int, K: int, D: int, out, ldout: int,
+              stream=None) -> None:
+    _check_feature(load().sad_blend(dtype, _ptr(F), ldf, n_sites, _ptr(ids), _ptr(weights), n_rows, K, D, _ptr(out),
+                                    ldout, _stream(stream)))
+
+
+def sad_blend_workspace_bytes(n_rows: int, K: int, n_sites: int, D: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check_feature(load().sad_blend_workspace_bytes(n_rows, K, n_sites, D, ctypes.byref(out)))
+    return out.value
+
+
+def sad_blend_backward(dtype: int, dout, lddout: int, F, ldf: int, n_sites: int, ids, weights, offsets, order,
+                       n_rows: int, K: int, D: int, dF, dweights, workspace, workspace_bytes: int,
+                       stream=None) -> None:
+    _check_feature(load().sad_blend_backward(dtype, _ptr(dout), lddout, _ptr(F), ldf, n_sites, _ptr(ids),
+                                             _ptr(weights), _ptr(offsets), _ptr(order), n_rows, K, D, _ptr(dF),
+                                             _ptr(dweights), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sad_layer_norm(dtype: int, x, ldx: int, gamma, beta, eps: float, n_rows: int, D: int, y, ldy: int, mean, rstd,
+                   stream=None) -> None:
+    _check_feature(load().sad_layer_norm(dtype, _ptr(x), ldx, _ptr(gamma), _ptr(beta), eps, n_rows, D, _ptr(y), ldy,
+                                         _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def sad_layer_norm_workspace_bytes(n_rows: int, D: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check_feature(load().sad_layer_norm_workspace_bytes(n_rows, D, ctypes.byref(out)))
+    return out.value
+
+
+def sad_layer_norm_backward(dtype: int, dy, lddy: int, x, ldx: int, gamma, mean, rstd, n_rows: int, D: int, dx,
+                            lddx: int, dgamma, dbeta, workspace, workspace_bytes: int, stream=None) -> None:
+    _check_feature(load().sad_layer_norm_backward(dtype, _ptr(dy), lddy, _ptr(x), ldx, _ptr(gamma), _ptr(mean),
+                                                  _ptr(rstd), n_rows, D, _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta),
+                                                  _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def sad_distill(dtype: int, logits, ld: int, teacher_ids, teacher_logits, row_weight, n_rows: int, V: int, M: int,
+                tau: float, loss, dlogits, lddlogits: int, stream=None) -> None:
+    _check_feature(load().sad_distill(dtype, _ptr(logits), ld, _ptr(teacher_ids), _ptr(teacher_logits),
+                                      _ptr(row_weight), n_rows, V, M, tau, _ptr(loss), _ptr(dlogits), lddlogits,
+                                      _stream(stream)))

@@ -20,6 +20,7 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
     "--expt-relaxed-constexpr",
+    "--threads", "0",  # the sources side by side
 ]
 
 

@@ -346,6 +346,15 @@ int sad_render(sad_ctx *ctx, float *image, sad_stream_t stream) {
     return cuda_status(ctx, sad::launch_render(ctx->dev, image, cs(stream)), "render");
 }
 
+int sad_blend_weights(sad_ctx *ctx, int32_t *ids, float *weights, sad_stream_t stream) {
+    int r = need_bound(ctx);
+    if (r) return r;
+    if (!ids || !weights) return fail(ctx, SAD_ERR_INVALID_ARG, "ids or weights is NULL");
+    if (!aligned16(ids) || !aligned16(weights))
+        return fail(ctx, SAD_ERR_INVALID_ARG, "ids or weights is not 16-byte aligned");
+    return cuda_status(ctx, sad::launch_blend_weights(ctx->dev, ids, weights, cs(stream)), "blend weights");
+}
+
 int sad_backward(sad_ctx *ctx, uint32_t flags, sad_stream_t stream) {
     int r = need_bound(ctx);
     if (r) return r;

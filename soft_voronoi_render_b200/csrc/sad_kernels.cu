@@ -8,6 +8,7 @@
 //   seed_*_kernel       a9  seed pass of a refresh
 //   propagate_kernel    a2/a3  one Jacobi candidate pass (+ injection)
 //   render_kernel       a4  softmax blend of the current candidates
+//   blend_weights_kernel  the same softmax, its ids and weights written out
 //   fixed_to_grads_kernel  adds the order-independent backward's 64-bit
 //                       fixed-point sums (the tile pass, sad_fused.cu) to
 //                       the gradients
@@ -698,6 +699,40 @@ __global__ void __launch_bounds__(TILE_THREADS) render_kernel(const float4 *__re
     }
 }
 
+// the render's weights and the ids that they belong to, one row of 8 a pixel
+__global__ void __launch_bounds__(TILE_THREADS) blend_weights_kernel(const float4 *__restrict__ rec,
+                                                                     const uint32_t *__restrict__ table, int H,
+                                                                     int W, TableGrid tg, int N,
+                                                                     int32_t *__restrict__ ids,
+                                                                     float *__restrict__ weights,
+                                                                     const Counters *__restrict__ c) {
+    const uint4 *in0 = reinterpret_cast<const uint4 *>(table + (size_t)c->cur * tg.PT * K);
+    const uint4 *in1 = in0 + tg.PT;
+    const int i = blockIdx.x * TILE_X + threadIdx.x;
+    const int j = blockIdx.y * TILE_Y + threadIdx.y;
+    if (i >= W || j >= H) return;
+    const size_t p = (size_t)j * W + i;
+    const size_t pt = tg.cell_of(i, j, p);
+    PixelSoftmax s;
+    unsigned dropped = 0;
+    const int nv = pixel_softmax(in0[pt], in1[pt], rec, (uint32_t)N, (float)i + 0.5f, (float)j + 0.5f, s, dropped);
+    const float iz = nv ? 1.0f / s.Z : 0.0f;
+    int32_t id[K];
+    float w[K];
+#pragma unroll
+    for (int q = 0; q < K; ++q) {
+        const bool in = s.valid >> q & 1u;
+        id[q] = in ? (int32_t)s.id[q] : -1;
+        w[q] = in ? s.l[q] * iz : 0.0f;
+    }
+    int4 *io = reinterpret_cast<int4 *>(ids) + p * 2;
+    float4 *wo = reinterpret_cast<float4 *>(weights) + p * 2;
+    io[0] = make_int4(id[0], id[1], id[2], id[3]);
+    io[1] = make_int4(id[4], id[5], id[6], id[7]);
+    wo[0] = make_float4(w[0], w[1], w[2], w[3]);
+    wo[1] = make_float4(w[4], w[5], w[6], w[7]);
+}
+
 // the deterministic backward's fixed-point sums, added to the gradients and
 // cleared for the next call
 __global__ void __launch_bounds__(SITE_THREADS) fixed_to_grads_kernel(unsigned long long *__restrict__ fixed,
@@ -997,6 +1032,12 @@ cudaError_t launch_jfa3x3(const Dev &d, int jump, cudaStream_t st, int score_cac
 cudaError_t launch_render(const Dev &d, float *image, cudaStream_t st) {
     render_kernel<<<tile_grid(d.H, d.W), dim3(TILE_X, TILE_Y), 0, st>>>(d.records, d.table, d.H, d.W, grid_of(d),
                                                                         d.N, image, host_counters(d));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_blend_weights(const Dev &d, int32_t *ids, float *weights, cudaStream_t st) {
+    blend_weights_kernel<<<tile_grid(d.H, d.W), dim3(TILE_X, TILE_Y), 0, st>>>(
+        d.records, d.table, d.H, d.W, grid_of(d), d.N, ids, weights, host_counters(d));
     return cudaGetLastError();
 }
 

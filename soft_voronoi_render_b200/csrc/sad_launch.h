@@ -52,6 +52,7 @@ cudaError_t launch_clear_table(const Dev &d, cudaStream_t st);
 cudaError_t launch_propagate(const Dev &d, int jump, int G, cudaStream_t st, int score_cache = 0);
 cudaError_t launch_pack_cand16(const Dev &d, cudaStream_t st);
 cudaError_t launch_render(const Dev &d, float *image, cudaStream_t st);
+cudaError_t launch_blend_weights(const Dev &d, int32_t *ids, float *weights, cudaStream_t st);
 cudaError_t launch_render_backward_det(const Dev &d, cudaStream_t st);
 cudaError_t launch_densify(const Dev &d, const DensifyArgs &a, cudaStream_t st);
 cudaError_t launch_tau_diffuse(const Dev &d, float lambda, cudaStream_t st);

@@ -1,0 +1,362 @@
+"""Feature fields: rows routed, blended, normalised and learned from a teacher.
+
+A site may carry D channels beside its colour; pixels (rows) blend the rows
+of their candidate sites (experts) with the render's softmax weights, which
+``Sad.blend_weights`` hands out.  Every function here checks its tensors,
+allocates its outputs where none are given and forwards to the C ABI
+(``include/sad.h``, "Feature fields") on the current stream of the tensors'
+device; no step of the computation runs in Python.
+
+Row matrices are 2-D tensors of float32, bfloat16 or float16 whose rows are
+consecutive elements (any row distance).  ids and places are dense int32, an id
+outside [0, n_sites) is an empty slot; weights are dense float32.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from ._lib import SAD_ERR_INVALID_ARG, SAD_ERR_UNSUPPORTED, SadError
+
+__all__ = ["Route", "blend", "blend_backward", "layer_norm", "layer_norm_backward", "distill", "FeatureField"]
+
+_TYPES = {torch.float32: _lib.SAD_F32, torch.bfloat16: _lib.SAD_BF16, torch.float16: _lib.SAD_F16}
+
+
+def _refuse(text: str):
+    raise SadError(SAD_ERR_INVALID_ARG, text)
+
+
+def _rows(name: str, x, shape=None, like=None):
+    """Checks a row matrix; returns its row distance."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _refuse(f"{name} must be a 2-D tensor")
+    if x.dtype not in _TYPES:
+        raise SadError(SAD_ERR_UNSUPPORTED, f"{name}: type {x.dtype} is not float32, bfloat16 or float16")
+    if not x.is_cuda:
+        _refuse(f"{name} must be on a CUDA device")
+    if like is not None and (x.dtype != like.dtype or x.device != like.device):
+        _refuse(f"{name} must have the type and the device of the other rows")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        _refuse(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    T, D = x.shape
+    if D < 1:
+        _refuse(f"{name} has no columns")
+    if (D > 1 and x.stride(1) != 1) or (T > 1 and x.stride(0) < D):
+        _refuse(f"{name}: a row's elements must be consecutive and rows must not overlap")
+    return x.stride(0) if T > 1 else D
+
+
+def _dense(name: str, x, dtype, shape, device):
+    if not isinstance(x, torch.Tensor) or x.dtype != dtype or tuple(x.shape) != tuple(shape):
+        _refuse(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    if x.device != device or not x.is_contiguous():
+        _refuse(f"{name} must be dense and on {device}")
+
+
+class _On:
+    """The tensors' device made current for one call, where it is not."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+class Route:
+    """Rows sorted by expert: the buffers of one routing, and the row
+    exchange that goes by it.
+
+    ``build`` fills ``offsets`` (n_sites + 1), ``order`` (n_rows * K) and
+    ``place`` (n_rows, K) for the ids it is given, in stream order; the calls
+    after it go by those until the next build.  A Route owns one workspace:
+    builds of one Route must not overlap on the GPU (use one Route per
+    stream, and one per captured graph that may run beside another).
+    """
+
+    def __init__(self, n_rows: int, K: int, n_sites: int, device="cuda"):
+        self.T, self.K, self.E = int(n_rows), int(K), int(n_sites)
+        ws = _lib.sad_route_workspace_bytes(self.T, self.K, self.E)
+        if not torch.cuda.is_available():
+            raise SadError(_lib.SAD_ERR_CUDA, "no CUDA device is available")
+        device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.offsets = torch.zeros(self.E + 1, **i32)
+        self.order = torch.full((self.T * self.K,), -1, **i32)
+        self.place = torch.full((self.T, self.K), -1, **i32)
+        self.device = self.offsets.device
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=device)
+
+    def build(self, ids) -> "Route":
+        _dense("ids", ids, torch.int32, (self.T, self.K), self.device)
+        with _On(self.device) as st:
+            _lib.sad_route(ids, self.T, self.K, self.E, self.offsets, self.order, self.place, self.workspace,
+                           self.workspace.numel(), st)
+        return self
+
+    def _weights(self, weights):
+        if weights is not None:
+            _dense("weights", weights, torch.float32, (self.T, self.K), self.device)
+
+    def _here(self, name, x):
+        if x.device != self.device:
+            _refuse(f"{name} is on {x.device}, the route on {self.device}")
+
+    def dispatch(self, x, weights=None, out=None):
+        """Rows out to their experts: (n_rows * K, D), row ``place[t, k]`` =
+        weights[t, k] x[t].  Rows behind the last pair (offsets[n_sites]) are
+        left as they were in ``out``, and undefined without it."""
+        ldx = _rows("x", x)
+        self._here("x", x)
+        D = x.shape[1]
+        if x.shape[0] != self.T:
+            _refuse(f"x has {x.shape[0]} rows, the route {self.T}")
+        self._weights(weights)
+        if out is None:
+            out = torch.empty((self.T * self.K, D), dtype=x.dtype, device=x.device)
+        ldo = _rows("out", out, (self.T * self.K, D), x)
+        with _On(self.device) as st:
+            _lib.sad_dispatch(_TYPES[x.dtype], x, ldx, weights, self.place, self.T, self.K, D, out, ldo, st)
+        return out
+
+    def dispatch_backward(self, dxs, x=None, weights=None, dx=None):
+        """(dx, dweights): dx[t] = sum of weights dxs[place]; dweights = <dxs[place],
+        x[t]> when x is given, else None."""
+        ld = _rows("dxs", dxs)
+        self._here("dxs", dxs)
+        D = dxs.shape[1]
+        if dxs.shape[0] != self.T * self.K:
+            _refuse(f"dxs has {dxs.shape[0]} rows, the route {self.T * self.K} pairs")
+        self._weights(weights)
+        ldx, dw = 0, None
+        if x is not None:
+            ldx = _rows("x", x, (self.T, D), dxs)
+            dw = torch.empty((self.T, self.K), dtype=torch.float32, device=x.device)
+        if dx is None:
+            dx = torch.empty((self.T, D), dtype=dxs.dtype, device=dxs.device)
+        lddx = _rows("dx", dx, (self.T, D), dxs)
+        with _On(self.device) as st:
+            _lib.sad_dispatch_backward(_TYPES[dxs.dtype], dxs, ld, x, ldx, weights, self.place, self.T, self.K, D, dx,
+                                       lddx, dw, st)
+        return dx, dw
+
+    def combine(self, y, weights=None, out=None):
+        """Rows back from their experts: out[t] = sum of weights[t, k]
+        y[place[t, k]]; a row without a pair gives 0."""
+        ldy = _rows("y", y)
+        self._here("y", y)
+        D = y.shape[1]
+        if y.shape[0] != self.T * self.K:
+            _refuse(f"y has {y.shape[0]} rows, the route {self.T * self.K} pairs")
+        self._weights(weights)
+        if out is None:
+            out = torch.empty((self.T, D), dtype=y.dtype, device=y.device)
+        ldo = _rows("out", out, (self.T, D), y)
+        with _On(self.device) as st:
+            _lib.sad_combine(_TYPES[y.dtype], y, ldy, weights, self.place, self.T, self.K, D, out, ldo, st)
+        return out
+
+    def combine_backward(self, dout, y=None, weights=None, dy=None):
+        """(dy, dweights): dy[place[t, k]] = weights[t, k] dout[t] (rows behind
+        the last pair as in ``dispatch``); dweights = <y[place], dout[t]> when
+        y is given, else None."""
+        ld = _rows("dout", dout)
+        self._here("dout", dout)
+        D = dout.shape[1]
+        if dout.shape[0] != self.T:
+            _refuse(f"dout has {dout.shape[0]} rows, the route {self.T}")
+        self._weights(weights)
+        ldy, dw = 0, None
+        if y is not None:
+            ldy = _rows("y", y, (self.T * self.K, D), dout)
+            dw = torch.empty((self.T, self.K), dtype=torch.float32, device=y.device)
+        if dy is None:
+            dy = torch.empty((self.T * self.K, D), dtype=dout.dtype, device=dout.device)
+        lddy = _rows("dy", dy, (self.T * self.K, D), dout)
+        with _On(self.device) as st:
+            _lib.sad_combine_backward(_TYPES[dout.dtype], dout, ld, y, ldy, weights, self.place, self.T, self.K, D,
+                                      dy, lddy, dw, st)
+        return dy, dw
+
+
+def _lists(ids, weights, device):
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        _refuse("ids must be a 2-D tensor")
+    _dense("ids", ids, torch.int32, ids.shape, device)
+    _dense("weights", weights, torch.float32, ids.shape, device)
+    return ids.shape
+
+
+def blend(F, ids, weights, out=None):
+    """Rows that a site's pixels share: out[t] = sum of weights[t, k]
+    F[ids[t, k]], F (n_sites, D)."""
+    ldf = _rows("F", F)
+    T, K = _lists(ids, weights, F.device)
+    E, D = F.shape
+    if out is None:
+        out = torch.empty((T, D), dtype=F.dtype, device=F.device)
+    ldo = _rows("out", out, (T, D), F)
+    with _On(F.device) as st:
+        _lib.sad_blend(_TYPES[F.dtype], F, ldf, E, ids, weights, T, K, D, out, ldo, st)
+    return out
+
+
+def blend_backward(dout, F, ids, weights, route=None, dF=None):
+    """(dF, dweights) of ``blend``: dF (n_sites, D) float32 sums each site's
+    pairs in order, by a Route built for these ids (None without one);
+    dweights (T, K) float32."""
+    ld, ldf = _rows("dout", dout), _rows("F", F, None, dout)
+    T, K = _lists(ids, weights, F.device)
+    E, D = F.shape
+    if tuple(dout.shape) != (T, D):
+        _refuse(f"dout has shape {tuple(dout.shape)}, expected {(T, D)}")
+    dev = F.device
+    dw = torch.empty((T, K), dtype=torch.float32, device=dev)
+    offsets = order = ws = None
+    nbytes = 0
+    if route is not None:
+        if (route.T, route.K, route.E) != (T, K, E) or route.device != dev:
+            _refuse("the route was made for other sizes or another device")
+        offsets, order = route.offsets, route.order
+        if dF is None:
+            dF = torch.empty((E, D), dtype=torch.float32, device=dev)
+        _dense("dF", dF, torch.float32, (E, D), dev)
+        nbytes = _lib.sad_blend_workspace_bytes(T, K, E, D)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    elif dF is not None:
+        _refuse("dF needs a route")
+    with _On(dev) as st:
+        _lib.sad_blend_backward(_TYPES[F.dtype], dout, ld, F, ldf, E, ids, weights, offsets, order, T, K, D, dF, dw,
+                                ws, nbytes, st)
+    return dF, dw
+
+
+def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, out=None):
+    """(y, mean, rstd) of every row of x; gamma and beta (D) float32 or None.
+    ``out`` may be x."""
+    ldx = _rows("x", x)
+    T, D = x.shape
+    dev = x.device
+    for name, v in (("gamma", gamma), ("beta", beta)):
+        if v is not None:
+            _dense(name, v, torch.float32, (D,), dev)
+    if out is None:
+        out = torch.empty((T, D), dtype=x.dtype, device=dev)
+    ldy = _rows("out", out, (T, D), x)
+    stats = torch.empty((2, T), dtype=torch.float32, device=dev)
+    mean, rstd = stats[0], stats[1]
+    with _On(dev) as st:
+        _lib.sad_layer_norm(_TYPES[x.dtype], x, ldx, gamma, beta, eps, T, D, out, ldy, mean, rstd, st)
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, want_affine: bool = True, dx=None):
+    """(dx, dgamma, dbeta) from the saved mean and rstd; without
+    ``want_affine`` the last two are None.  ``dx`` may be dy."""
+    ld, ldx = _rows("dy", dy), _rows("x", x, None, dy)
+    T, D = x.shape
+    dev = x.device
+    if tuple(dy.shape) != (T, D):
+        _refuse(f"dy has shape {tuple(dy.shape)}, expected {(T, D)}")
+    if gamma is not None:
+        _dense("gamma", gamma, torch.float32, (D,), dev)
+    _dense("mean", mean, torch.float32, (T,), dev)
+    _dense("rstd", rstd, torch.float32, (T,), dev)
+    if dx is None:
+        dx = torch.empty((T, D), dtype=x.dtype, device=dev)
+    lddx = _rows("dx", dx, (T, D), x)
+    dgamma = dbeta = ws = None
+    nbytes = 0
+    if want_affine:
+        grads = torch.empty((2, D), dtype=torch.float32, device=dev)
+        dgamma, dbeta = grads[0], grads[1]
+        nbytes = _lib.sad_layer_norm_workspace_bytes(T, D)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with _On(dev) as st:
+        _lib.sad_layer_norm_backward(_TYPES[x.dtype], dy, ld, x, ldx, gamma, mean, rstd, T, D, dx, lddx, dgamma,
+                                     dbeta, ws, nbytes, st)
+    return dx, dgamma, dbeta
+
+
+def distill(logits, teacher_ids, teacher_logits, temperature: float = 1.0, row_weight=None, want_grad: bool = True,
+            dlogits=None):
+    """(loss (T), dlogits (T, V) or None): the divergence of softmax(logits /
+    temperature) from the teacher's over its top classes, times temperature^2
+    and the row's weight, and its gradient (sad_distill in include/sad.h has
+    the formulas and what empty rows give).  ``dlogits`` may be logits."""
+    ld = _rows("logits", logits)
+    T, V = logits.shape
+    dev = logits.device
+    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2 or teacher_ids.shape[0] != T:
+        _refuse(f"teacher_ids must have {T} rows")
+    M = teacher_ids.shape[1]
+    _dense("teacher_ids", teacher_ids, torch.int32, (T, M), dev)
+    _dense("teacher_logits", teacher_logits, torch.float32, (T, M), dev)
+    if row_weight is not None:
+        _dense("row_weight", row_weight, torch.float32, (T,), dev)
+    lddz = 0
+    if dlogits is not None or want_grad:
+        if dlogits is None:
+            dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev)
+        lddz = _rows("dlogits", dlogits, (T, V), logits)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    with _On(dev) as st:
+        _lib.sad_distill(_TYPES[logits.dtype], logits, ld, teacher_ids, teacher_logits, row_weight, T, V, M,
+                         float(temperature), loss, dlogits, lddz, st)
+    return loss, dlogits
+
+
+class FeatureField:
+    """D channels for every site of a ``Sad``, blended per pixel by the
+    render's weights and layer-normalised (convex blending shrinks rows where
+    unlike sites meet; the norm undoes it).
+
+    ``features`` (N, D), ``gamma`` and ``beta`` (D) are float32 and the
+    caller's to optimise; ``loss_and_grads`` fills ``grad_features``,
+    ``grad_gamma`` and ``grad_beta``.  ``update_lists`` takes the current
+    candidate lists; call it after the lists or the sites changed.  The sites
+    themselves are fitted by the colour loss and not moved here.
+    """
+
+    def __init__(self, sad, D: int, seed: int = 1, eps: float = 1e-5):
+        if D < 1:
+            _refuse(f"D = {D} is below 1")
+        self.sad, self.D, self.eps = sad, int(D), float(eps)
+        f32 = dict(dtype=torch.float32, device=sad.device)
+        gen = torch.Generator(sad.device).manual_seed(seed)
+        self.features = torch.randn((sad.N, self.D), generator=gen, **f32).mul_(0.01)
+        self.gamma, self.beta = torch.ones(self.D, **f32), torch.zeros(self.D, **f32)
+        self.grad_features = torch.zeros((sad.N, self.D), **f32)
+        self.grad_gamma = self.grad_beta = None
+        self.ids = torch.full((sad.P, 8), -1, dtype=torch.int32, device=sad.device)
+        self.weights = torch.zeros((sad.P, 8), **f32)
+        self.route = Route(sad.P, 8, sad.N, sad.device)
+
+    def update_lists(self, route: bool = True) -> None:
+        """The lists' ids and weights, and (for fitting) their routing."""
+        self.sad.blend_weights(self.ids, self.weights)
+        if route:
+            self.route.build(self.ids)
+
+    def render(self):
+        """The field's (P, D) rows: class logits, or an embedding."""
+        return layer_norm(blend(self.features, self.ids, self.weights), self.gamma, self.beta, self.eps)[0]
+
+    def loss_and_grads(self, teacher_ids, teacher_logits, temperature: float = 1.0, row_weight=None):
+        """The pixels' distillation losses (P); the D channels are the
+        teacher's classes.  Gradients are those of the losses' sum."""
+        x = blend(self.features, self.ids, self.weights)
+        y, mean, rstd = layer_norm(x, self.gamma, self.beta, self.eps)
+        loss, dy = distill(y, teacher_ids, teacher_logits, temperature, row_weight, dlogits=y)
+        dx, self.grad_gamma, self.grad_beta = layer_norm_backward(dy, x, self.gamma, mean, rstd, dx=dy)
+        blend_backward(dx, self.features, self.ids, self.weights, self.route, dF=self.grad_features)
+        return loss

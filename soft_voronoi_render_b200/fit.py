@@ -11,6 +11,9 @@ differentiates the cached lists (sad_fit_pass_cached), the infrequent
 candidate update of the pages' section B.3; ``passes_per_update`` jump-1
 passes run at each such update (the last one fused with the render).  The
 site count stays on the device.
+
+``run_features`` fits a feature field on a fitted diagram from a teacher's top
+logits.
 """
 from __future__ import annotations
 
@@ -92,3 +95,28 @@ def run(sad, sched: Schedule, on_event=None, graphs: bool = True) -> dict:
         eager += 1
         it += 1
     return {"eager_iterations": eager, "graph_replays": replays, "chunk": chunk}
+
+
+def run_features(field_, teacher_ids, teacher_logits, iterations: int = 100, lr: float = 0.05,
+                 temperature: float = 1.0, row_weight=None) -> list:
+    """Fit a ``features.FeatureField`` to a teacher's top classes per pixel
+    (teacher_ids (P, M) int32, teacher_logits (P, M) float32) on the sites and
+    lists as they are: every iteration blends, normalises and distils all
+    pixels, takes the gradients back to the sites' rows and makes an Adam step
+    on features, gamma and beta.  row_weight (P) float32 masks or weights
+    pixels.  Returns the mean loss per pixel of every iteration."""
+    import torch
+
+    leaves = [field_.features, field_.gamma, field_.beta]
+    opt = torch.optim.Adam(leaves, lr=lr)
+    field_.update_lists()
+    losses = []
+    for _ in range(iterations):
+        loss = field_.loss_and_grads(teacher_ids, teacher_logits, temperature, row_weight)
+        for leaf, grad in zip(leaves, (field_.grad_features, field_.grad_gamma, field_.grad_beta)):
+            leaf.grad = grad
+        opt.step()
+        losses.append(loss.mean())
+    for leaf in leaves:
+        leaf.grad = None
+    return torch.stack(losses).tolist() if losses else []
