@@ -8,6 +8,14 @@
 //   segments dF[e] = sum_{j of e} w_j G[t_j]  blend's dF
 //
 // All three move rows; the arithmetic is one multiply-add per element moved.
+//
+// gather and spread: a group of L lanes (the power of two that covers a row
+// in 16-byte pieces, at most a warp) takes one row, reads its K ids and
+// weights, and has all K rows' loads in flight at once; wider rows loop, and
+// where there are few wide rows the warps of a block share one.  The K dot
+// products are summed over the group by halving: each step of the butterfly
+// also halves the number of sums a lane keeps, 7 + log2(L / 8) shuffles
+// instead of 8 log2 L.
 #include "sad_features.h"
 #include "sad_rows.cuh"
 
@@ -16,153 +24,418 @@ namespace sad {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
 constexpr int K_MAX = 8;
 
-// a group of 32 lanes per row
-template <typename T, int VEC, bool SUM, bool DOT>
+// the K ids and weights of row t; ids beyond K are empty slots
+template <bool FULL>
+__device__ __forceinline__ void load_slots(const int32_t *__restrict__ at, const float *__restrict__ w, long long t,
+                                           int K, bool in, uint32_t (&id)[K_MAX], float (&wt)[K_MAX]) {
+    if (FULL) {  // K = 8, 16-byte aligned lists
+        int4 a = make_int4(-1, -1, -1, -1), b = a;
+        float4 u = make_float4(1.0f, 1.0f, 1.0f, 1.0f), v = u;
+        if (in) {
+            const int4 *p = reinterpret_cast<const int4 *>(at) + t * 2;
+            a = __ldg(p);
+            b = __ldg(p + 1);
+            if (w) {
+                const float4 *q = reinterpret_cast<const float4 *>(w) + t * 2;
+                u = __ldg(q);
+                v = __ldg(q + 1);
+            }
+        }
+        id[0] = a.x, id[1] = a.y, id[2] = a.z, id[3] = a.w, id[4] = b.x, id[5] = b.y, id[6] = b.z, id[7] = b.w;
+        wt[0] = u.x, wt[1] = u.y, wt[2] = u.z, wt[3] = u.w, wt[4] = v.x, wt[5] = v.y, wt[6] = v.z, wt[7] = v.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < K_MAX; ++k) {
+            const bool on = in && k < K;
+            id[k] = on ? (uint32_t)__ldg(at + t * K + k) : 0xffffffffu;
+            wt[k] = on && w ? __ldg(w + t * K + k) : 1.0f;
+        }
+    }
+}
+
+// sums v[0..7] over the L lanes of a group; afterwards lane `first + i` slots
+// belong to this lane: v[i], i < count, is the sum of slot first + i
+__device__ __forceinline__ void group_sums(float (&v)[K_MAX], int L, int lane, int &first, int &count) {
+    first = 0;
+    count = K_MAX;
+    int o = L >> 1;
+#pragma unroll
+    for (int half = K_MAX / 2; half; half >>= 1) {
+        if (o) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+            first += up ? half : 0;
+            count = half;
+            o >>= 1;
+        }
+    }
+    for (; o; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+}
+
+// Where a lane works: its row t, the column of its first piece and the
+// distance to its next.  ROW_PER_BLOCK: all warps share row blockIdx.x.
+template <int VEC, bool ROW_PER_BLOCK> struct Lanes {
+    int L, lane;       // lanes of a group, this one's number in it
+    long long t;
+    bool in;
+    int c0, step;
+    __device__ __forceinline__ Lanes(int log_l, long long n_rows) {
+        if (ROW_PER_BLOCK) {
+            L = 32;
+            lane = threadIdx.x & 31;
+            t = blockIdx.x;
+            c0 = threadIdx.x * VEC;
+            step = THREADS * VEC;
+        } else {
+            L = 1 << log_l;
+            lane = threadIdx.x & (L - 1);
+            t = ((long long)blockIdx.x * THREADS + threadIdx.x) >> log_l;
+            c0 = lane * VEC;
+            step = L * VEC;
+        }
+        in = t < n_rows;
+    }
+};
+
+// writes the dot products of the group's row; dot[k] of empty slots is 0
+template <bool ROW_PER_BLOCK>
+__device__ __forceinline__ void finish_dots(float (&dot)[K_MAX], int L, int lane, long long t, bool in, int K,
+                                            float *__restrict__ dots) {
+    int first, count;
+    group_sums(dot, L, lane, first, count);
+    if (ROW_PER_BLOCK) {
+        __shared__ float part[WARPS][K_MAX];
+        // 32 lanes: 8 slots over 4 lanes each, one sum a lane
+        if ((lane & 3) == 0) part[threadIdx.x >> 5][first] = dot[0];
+        __syncthreads();
+        if (threadIdx.x < K) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < WARPS; ++q) s += part[q][threadIdx.x];
+            dots[t * K + threadIdx.x] = s;
+        }
+        return;
+    }
+    // of the lanes that hold the same sum (L > 8) the first writes
+    if (!in || (L > 8 && (lane & (L / 8 - 1)))) return;
+#pragma unroll
+    for (int i = 0; i < K_MAX; ++i)
+        if (i < count && first + i < K) dots[t * K + first + i] = dot[i];
+}
+
+template <typename T, int VEC, bool FULL, bool SUM, bool DOT, bool ROW_PER_BLOCK>
 __global__ void __launch_bounds__(THREADS) gather_kernel(const T *__restrict__ R, long long ldr,
                                                          const int32_t *__restrict__ at, uint32_t n_at,
                                                          const float *__restrict__ w, const T *__restrict__ G,
-                                                         long long ldg, long long n_rows, int K, int D,
+                                                         long long ldg, long long n_rows, int K, int D, int log_l,
                                                          T *__restrict__ out, long long ldo,
                                                          float *__restrict__ dots) {
-    const int lane = threadIdx.x & 31;
-    const long long t = ((long long)blockIdx.x * THREADS + threadIdx.x) >> 5;
-    if (t >= n_rows) return;
+    const Lanes<VEC, ROW_PER_BLOCK> me(log_l, n_rows);
     uint32_t id[K_MAX];
-    float wt[K_MAX], dot[K_MAX];
+    float wt[K_MAX], dot[K_MAX] = {};
+    load_slots<FULL>(at, SUM ? w : nullptr, me.t, K, me.in, id, wt);
+    if (me.in) {
+        for (int c = me.c0; c < D; c += me.step) {
+            Pack<T, VEC> p[K_MAX];
 #pragma unroll
-    for (int k = 0; k < K_MAX; ++k) {
-        id[k] = k < K ? (uint32_t)at[t * K + k] : 0xffffffffu;
-        wt[k] = SUM && id[k] < n_at ? (w ? w[t * K + k] : 1.0f) : 0.0f;
-        dot[k] = 0.0f;
-    }
-    for (int c = lane * VEC; c < D; c += 32 * VEC) {
-        float acc[VEC] = {}, g[VEC] = {};
-        if (DOT) {
-            const Pack<T, VEC> p = load_pack<T, VEC>(G + t * ldg + c);
+            for (int k = 0; k < K_MAX; ++k)
+                if (id[k] < n_at) p[k] = load_pack<T, VEC>(R + (long long)id[k] * ldr + c);
+            float acc[VEC] = {};
+            Pack<T, VEC> g;
+            if (DOT) g = load_pack<T, VEC>(G + me.t * ldg + c);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) g[i] = p.get(i);
-        }
+            for (int k = 0; k < K_MAX; ++k) {
+                if (id[k] >= n_at) continue;
 #pragma unroll
-        for (int k = 0; k < K_MAX; ++k) {
-            if (id[k] >= n_at) continue;
-            const Pack<T, VEC> p = load_pack<T, VEC>(R + (long long)id[k] * ldr + c);
+                for (int i = 0; i < VEC; ++i) {
+                    if (SUM) acc[i] = fmaf(wt[k], p[k].get(i), acc[i]);
+                    if (DOT) dot[k] = fmaf(p[k].get(i), g.get(i), dot[k]);
+                }
+            }
+            if (SUM) {
+                Pack<T, VEC> o;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                if (SUM) acc[i] = fmaf(wt[k], p.get(i), acc[i]);
-                if (DOT) dot[k] = fmaf(p.get(i), g[i], dot[k]);
+                for (int i = 0; i < VEC; ++i) o.set(i, acc[i]);
+                store_pack<T, VEC>(out + me.t * ldo + c, o);
             }
         }
-        if (SUM) {
-            Pack<T, VEC> p;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) p.set(i, acc[i]);
-            store_pack<T, VEC>(out + t * ldo + c, p);
-        }
     }
-    if (DOT) {
-#pragma unroll
-        for (int k = 0; k < K_MAX; ++k) {
-            const float s = group_sum<32>(dot[k]);
-            if (lane == 0 && k < K) dots[t * K + k] = s;
-        }
-    }
+    if (DOT) finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
 }
 
-template <typename T, int VEC, bool DOT>
+template <typename T, int VEC, bool FULL, bool DOT, bool ROW_PER_BLOCK>
 __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X, long long ldx,
                                                          const int32_t *__restrict__ at, uint32_t n_at,
                                                          const float *__restrict__ w, const T *__restrict__ R,
-                                                         long long ldr, long long n_rows, int K, int D,
+                                                         long long ldr, long long n_rows, int K, int D, int log_l,
                                                          T *__restrict__ S, long long lds,
                                                          float *__restrict__ dots) {
-    const int lane = threadIdx.x & 31;
-    const long long t = ((long long)blockIdx.x * THREADS + threadIdx.x) >> 5;
-    if (t >= n_rows) return;
+    const Lanes<VEC, ROW_PER_BLOCK> me(log_l, n_rows);
     uint32_t id[K_MAX];
-    float wt[K_MAX], dot[K_MAX];
-#pragma unroll
-    for (int k = 0; k < K_MAX; ++k) {
-        id[k] = k < K ? (uint32_t)at[t * K + k] : 0xffffffffu;
-        wt[k] = id[k] < n_at ? (w ? w[t * K + k] : 1.0f) : 0.0f;
-        dot[k] = 0.0f;
-    }
-    for (int c = lane * VEC; c < D; c += 32 * VEC) {
-        const Pack<T, VEC> x = load_pack<T, VEC>(X + t * ldx + c);
-#pragma unroll
-        for (int k = 0; k < K_MAX; ++k) {
-            if (id[k] >= n_at) continue;
-            Pack<T, VEC> p;
+    float wt[K_MAX], dot[K_MAX] = {};
+    load_slots<FULL>(at, w, me.t, K, me.in, id, wt);
+    if (me.in) {
+        for (int c = me.c0; c < D; c += me.step) {
+            Pack<T, VEC> p[K_MAX];
             if (DOT) {
-                p = load_pack<T, VEC>(R + (long long)id[k] * ldr + c);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) dot[k] = fmaf(p.get(i), x.get(i), dot[k]);
+                for (int k = 0; k < K_MAX; ++k)
+                    if (id[k] < n_at) p[k] = load_pack<T, VEC>(R + (long long)id[k] * ldr + c);
             }
+            const Pack<T, VEC> x = load_pack<T, VEC>(X + me.t * ldx + c);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) p.set(i, wt[k] * x.get(i));
-            store_pack<T, VEC>(S + (long long)id[k] * lds + c, p);
+            for (int k = 0; k < K_MAX; ++k) {
+                if (id[k] >= n_at) continue;
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (DOT) dot[k] = fmaf(p[k].get(i), x.get(i), dot[k]);
+                    o.set(i, wt[k] * x.get(i));
+                }
+                store_pack<T, VEC>(S + (long long)id[k] * lds + c, o);
+            }
         }
     }
-    if (DOT) {
-#pragma unroll
-        for (int k = 0; k < K_MAX; ++k) {
-            const float s = group_sum<32>(dot[k]);
-            if (lane == 0 && k < K) dots[t * K + k] = s;
-        }
-    }
+    if (DOT) finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
 }
 
-// a warp per site
+// ---------------------------------------------------------------------------
+// segment sums
+//
+// The sorted pairs are cut into chunks of C positions, a warp each, whatever
+// the experts' shares are.  A warp walks its chunk's runs of one expert: 32
+// pairs and weights a step, the rows by S = 32 / L groups side by side, and
+// joins the groups at the run's end.  A run that is all of its expert's pairs
+// goes to dF; one that is cut at the chunk's start or end goes to one of the
+// chunk's two partial rows, which join_kernel adds up in order.
+// ---------------------------------------------------------------------------
+
+// the last e in [0, E) with offsets[e] <= s, for s below offsets[E]
+__device__ __forceinline__ int expert_at(const int32_t *__restrict__ offsets, int E, uint32_t s) {
+    int lo = 0, hi = E;  // offsets[lo] <= s < offsets[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((uint32_t)__ldg(offsets + mid) <= s) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 template <typename T, int VEC>
 __global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ G, long long ldg,
                                                           const float *__restrict__ w,
                                                           const int32_t *__restrict__ offsets,
                                                           const int32_t *__restrict__ order, uint32_t n, int K, int E,
-                                                          int D, float *__restrict__ dF) {
-    const int lane = threadIdx.x & 31;
-    const long long e = ((long long)blockIdx.x * THREADS + threadIdx.x) >> 5;
-    if (e >= E) return;
-    const uint32_t lo = min((uint32_t)offsets[e], n), hi = min((uint32_t)offsets[e + 1], n);
-    for (int c = lane * VEC; c < D; c += 32 * VEC) {
-        float acc[VEC] = {};
-        for (uint32_t s = lo; s < hi; ++s) {
-            const uint32_t j = (uint32_t)order[s];
-            if (j >= n) continue;
-            const float wj = w[j];
-            const Pack<T, VEC> p = load_pack<T, VEC>(G + (long long)(j / K) * ldg + c);
+                                                          int D, int log_l, uint32_t C, uint32_t chunks,
+                                                          float *__restrict__ dF, float *__restrict__ partial) {
+    const int L = 1 << log_l, S = 32 >> log_l;
+    const int lane = threadIdx.x & 31, sub = lane >> log_l, in_row = lane & (L - 1);
+    const uint32_t chunk = (uint32_t)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
+    if (chunk >= chunks) return;
+    const uint32_t total = min((uint32_t)__ldg(offsets + E), n);
+    const uint32_t lo = chunk * C;
+    if (lo >= total) return;
+    const uint32_t hi = min(lo + C, total);
+    const int first = expert_at(offsets, E, lo);
+    for (int slab = blockIdx.y * 32 * VEC; slab < D; slab += gridDim.y * 32 * VEC) {
+        const int c = slab + in_row * VEC;
+        const bool col = c < D;
+        int e = first;
+        uint32_t a = lo;
+        while (a < hi && e < E) {
+            const uint32_t end = min((uint32_t)__ldg(offsets + e + 1), total);
+            if (end <= a) {
+                ++e;
+                continue;
+            }
+            const uint32_t b = min(end, hi);
+            float acc[VEC] = {};
+            for (uint32_t s = a; s < b; s += 32) {
+                uint32_t row = 0;
+                float wj = 0.0f;
+                if (s + lane < b) {
+                    const uint32_t j = (uint32_t)__ldg(order + s + lane);
+                    if (j < n) {
+                        row = j / (uint32_t)K;
+                        wj = __ldg(w + j);
+                    }
+                }
+                const uint32_t left = min(b - s, 32u);
+                for (uint32_t q = 0; q < left; q += 4 * S) {
+                    Pack<T, VEC> p[4];
+                    float wq[4];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] = fmaf(wj, p.get(i), acc[i]);
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t at = q + u * S + sub;
+                        const uint32_t r = __shfl_sync(0xffffffffu, row, at & 31);
+                        wq[u] = __shfl_sync(0xffffffffu, wj, at & 31);
+                        if (at < left && col) p[u] = load_pack<T, VEC>(G + (long long)r * ldg + c);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (q + u * S + sub < left && col) {
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) acc[i] = fmaf(wq[u], p[u].get(i), acc[i]);
+                        }
+                    }
+                }
+            }
+            for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+            }
+            if (sub == 0 && col) {
+                const bool whole = (uint32_t)__ldg(offsets + e) == a && end == b;
+                float *to = whole ? dF + (long long)e * D + c
+                                  : partial + ((size_t)2 * chunk + (a == lo ? 0 : 1)) * D + c;
+                Pack<float, VEC % 4 ? VEC : 4> f;
+                constexpr int FV = VEC % 4 ? VEC : 4;
+#pragma unroll
+                for (int i = 0; i < VEC; i += FV) {
+#pragma unroll
+                    for (int v = 0; v < FV; ++v) f.v[v] = acc[i + v];
+                    // dF may start anywhere on 4 bytes
+                    if (FV == 4 && (reinterpret_cast<uintptr_t>(to + i) & 15) == 0) store_pack<float, FV>(to + i, f);
+                    else
+                        for (int v = 0; v < FV; ++v) to[i + v] = f.v[v];
+                }
+            }
+            a = b;
+            ++e;
         }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dF[e * D + c + i] = acc[i];
     }
 }
 
-// rows can be read 16 bytes at a time: base and row distance on 16-byte
-// boundaries (D need not be: the caller adds that)
-bool wide(const void *p, long long ld, int bytes) {
-    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * bytes & 15) == 0);
+// a block per chunk: where an expert's pairs start in the chunk (or at its
+// first position) and reach beyond it, adds up that expert's partial rows
+__global__ void __launch_bounds__(THREADS) join_kernel(const int32_t *__restrict__ offsets, uint32_t n, int E, int D,
+                                                       uint32_t C, const float *__restrict__ partial,
+                                                       float *__restrict__ dF) {
+    __shared__ int expert;
+    __shared__ float part[WARPS][33];
+    const uint32_t chunk = blockIdx.x, lo = chunk * C;
+    const uint32_t total = min((uint32_t)__ldg(offsets + E), n);
+    if (total <= lo || total - lo <= C) return;  // nothing reaches beyond the last chunk
+    if (threadIdx.x == 0) expert = expert_at(offsets, E, lo + C - 1);
+    __syncthreads();
+    const int e = expert;
+    const uint32_t from = (uint32_t)__ldg(offsets + e), end = min((uint32_t)__ldg(offsets + e + 1), total);
+    if (from < lo || end <= lo + C) return;  // started earlier, or ends here
+    const uint32_t last = (end - 1) / C;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        const int c = c0 + lane;
+        float s = 0.0f;
+        if (c < D) {
+            // rows chunk .. last in runs of a warp each
+            const uint32_t count = last - chunk + 1, each = (count + WARPS - 1) / WARPS;
+            const uint32_t q0 = chunk + warp * each, q1 = min(q0 + each, last + 1);
+#pragma unroll 8
+            for (uint32_t q = q0; q < q1; ++q) {
+                const int slot = q == chunk && from != lo ? 1 : 0;
+                s += __ldg(partial + ((size_t)2 * q + slot) * D + c);
+            }
+        }
+        part[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && c < D) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < WARPS; ++q) sum += part[q][lane];
+            dF[(long long)e * D + c] = sum;
+        }
+        __syncthreads();
+    }
 }
 
-unsigned warp_blocks(long long rows) { return (unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32)); }
+// the largest piece that base, row distance and D allow: 16 bytes, 4 bytes
+// (16-bit types) or one element
+int piece_bytes(const void *p, long long ld, int D, int bytes) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * bytes) | (uintptr_t)((long long)D * bytes);
+    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : bytes;
+}
+
+int ceil_log2(int v) {
+    int l = 0;
+    while ((1 << l) < v) ++l;
+    return l;
+}
+
+// lanes for a row of D elements in pieces of VEC, at most a warp
+int group_log(int D, int vec) {
+    const int pieces = (D + vec - 1) / vec;
+    return pieces >= 32 ? 5 : ceil_log2(pieces);
+}
+
+struct Shape {
+    unsigned blocks;
+    int log_l;
+    bool row_per_block;
+};
+
+// A row's pieces beyond a warp's 32 are looped over by that warp, unless the
+// rows are too few to give every SM eight warps: then a block shares a row.
+Shape shape_of(long long n, int D, int vec) {
+    Shape s;
+    s.log_l = group_log(D, vec);
+    s.row_per_block = D > 32 * vec && n < 148 * 8;
+    const long long per_block = s.row_per_block ? 1 : THREADS >> s.log_l;
+    s.blocks = (unsigned)((n + per_block - 1) / per_block);
+    return s;
+}
+
+template <typename T, int VEC, bool FULL, bool SUM, bool DOT>
+void gather_launch(const Shape &s, const T *R, long long ldr, const int32_t *at, uint32_t n_at, const float *w,
+                   const T *G, long long ldg, long long n, int K, int D, T *out, long long ldo, float *dots,
+                   cudaStream_t st) {
+    if (s.row_per_block)
+        gather_kernel<T, VEC, FULL, SUM, DOT, true><<<s.blocks, THREADS, 0, st>>>(R, ldr, at, n_at, w, G, ldg, n, K, D,
+                                                                                  5, out, ldo, dots);
+    else
+        gather_kernel<T, VEC, FULL, SUM, DOT, false><<<s.blocks, THREADS, 0, st>>>(R, ldr, at, n_at, w, G, ldg, n, K,
+                                                                                   D, s.log_l, out, ldo, dots);
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <typename T, int VEC>
 cudaError_t gather(RowsIn rows, const int32_t *at, long long n_at, const float *w, RowsIn other, long long n, int K,
                    int D, RowsOut out, float *dots, cudaStream_t st) {
     const T *r = static_cast<const T *>(rows.p), *g = static_cast<const T *>(other.p);
     T *o = static_cast<T *>(out.p);
-    const unsigned blocks = warp_blocks(n);
-    if (o && dots)
-        gather_kernel<T, VEC, true, true><<<blocks, THREADS, 0, st>>>(r, rows.ld, at, (uint32_t)n_at, w, g, other.ld,
-                                                                      n, K, D, o, out.ld, dots);
-    else if (o)
-        gather_kernel<T, VEC, true, false><<<blocks, THREADS, 0, st>>>(r, rows.ld, at, (uint32_t)n_at, w, g, other.ld,
-                                                                       n, K, D, o, out.ld, dots);
-    else
-        gather_kernel<T, VEC, false, true><<<blocks, THREADS, 0, st>>>(r, rows.ld, at, (uint32_t)n_at, w, g, other.ld,
-                                                                       n, K, D, o, out.ld, dots);
+    const Shape s = shape_of(n, D, VEC);
+    const uint32_t m = (uint32_t)n_at;
+    const bool full = K == K_MAX && aligned16(at) && aligned16(w);
+    if (o && dots) {
+        if (full) gather_launch<T, VEC, true, true, true>(s, r, rows.ld, at, m, w, g, other.ld, n, K, D, o, out.ld, dots, st);
+        else gather_launch<T, VEC, false, true, true>(s, r, rows.ld, at, m, w, g, other.ld, n, K, D, o, out.ld, dots, st);
+    } else if (o) {
+        if (full) gather_launch<T, VEC, true, true, false>(s, r, rows.ld, at, m, w, g, 0, n, K, D, o, out.ld, dots, st);
+        else gather_launch<T, VEC, false, true, false>(s, r, rows.ld, at, m, w, g, 0, n, K, D, o, out.ld, dots, st);
+    } else {
+        if (full) gather_launch<T, VEC, true, false, true>(s, r, rows.ld, at, m, w, g, other.ld, n, K, D, o, 0, dots, st);
+        else gather_launch<T, VEC, false, false, true>(s, r, rows.ld, at, m, w, g, other.ld, n, K, D, o, 0, dots, st);
+    }
     return cudaGetLastError();
+}
+
+template <typename T, int VEC, bool FULL, bool DOT>
+void spread_launch(const Shape &s, const T *X, long long ldx, const int32_t *at, uint32_t n_at, const float *w,
+                   const T *R, long long ldr, long long n, int K, int D, T *S, long long lds, float *dots,
+                   cudaStream_t st) {
+    if (s.row_per_block)
+        spread_kernel<T, VEC, FULL, DOT, true><<<s.blocks, THREADS, 0, st>>>(X, ldx, at, n_at, w, R, ldr, n, K, D, 5,
+                                                                             S, lds, dots);
+    else
+        spread_kernel<T, VEC, FULL, DOT, false><<<s.blocks, THREADS, 0, st>>>(X, ldx, at, n_at, w, R, ldr, n, K, D,
+                                                                              s.log_l, S, lds, dots);
 }
 
 template <typename T, int VEC>
@@ -170,47 +443,67 @@ cudaError_t spread(RowsIn x, const int32_t *at, long long n_at, const float *w, 
                    int D, RowsOut to, float *dots, cudaStream_t st) {
     const T *xp = static_cast<const T *>(x.p), *r = static_cast<const T *>(rows.p);
     T *o = static_cast<T *>(to.p);
-    const unsigned blocks = warp_blocks(n);
-    if (dots)
-        spread_kernel<T, VEC, true><<<blocks, THREADS, 0, st>>>(xp, x.ld, at, (uint32_t)n_at, w, r, rows.ld, n, K, D,
-                                                                o, to.ld, dots);
-    else
-        spread_kernel<T, VEC, false><<<blocks, THREADS, 0, st>>>(xp, x.ld, at, (uint32_t)n_at, w, r, rows.ld, n, K, D,
-                                                                 o, to.ld, dots);
+    const Shape s = shape_of(n, D, VEC);
+    const uint32_t m = (uint32_t)n_at;
+    const bool full = K == K_MAX && aligned16(at) && aligned16(w);
+    if (dots) {
+        if (full) spread_launch<T, VEC, true, true>(s, xp, x.ld, at, m, w, r, rows.ld, n, K, D, o, to.ld, dots, st);
+        else spread_launch<T, VEC, false, true>(s, xp, x.ld, at, m, w, r, rows.ld, n, K, D, o, to.ld, dots, st);
+    } else {
+        if (full) spread_launch<T, VEC, true, false>(s, xp, x.ld, at, m, w, r, 0, n, K, D, o, to.ld, dots, st);
+        else spread_launch<T, VEC, false, false>(s, xp, x.ld, at, m, w, r, 0, n, K, D, o, to.ld, dots, st);
+    }
     return cudaGetLastError();
 }
+
+// calls f<T, VEC> with the piece that all matrices allow
+#define BY_PIECE(T, bytes, f, ...)                                        \
+    ((bytes) == 16 ? f<T, 16 / sizeof(T)>(__VA_ARGS__)                    \
+                   : (bytes) == 4 ? f<T, 4 / sizeof(T)>(__VA_ARGS__) : f<T, 1>(__VA_ARGS__))
 
 template <typename T>
 cudaError_t gather_typed(RowsIn rows, const int32_t *at, long long n_at, const float *w, RowsIn other, long long n,
                          int K, int D, RowsOut out, float *dots, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    if (D % V == 0 && wide(rows.p, rows.ld, sizeof(T)) && (!dots || wide(other.p, other.ld, sizeof(T))) &&
-        wide(out.p, out.ld, sizeof(T)))
-        return gather<T, V>(rows, at, n_at, w, other, n, K, D, out, dots, st);
-    return gather<T, 1>(rows, at, n_at, w, other, n, K, D, out, dots, st);
+    int b = piece_bytes(rows.p, rows.ld, D, sizeof(T));
+    if (dots) b = min(b, piece_bytes(other.p, other.ld, D, sizeof(T)));
+    if (out.p) b = min(b, piece_bytes(out.p, out.ld, D, sizeof(T)));
+    return BY_PIECE(T, b, gather, rows, at, n_at, w, other, n, K, D, out, dots, st);
 }
 
 template <typename T>
 cudaError_t spread_typed(RowsIn x, const int32_t *at, long long n_at, const float *w, RowsIn rows, long long n, int K,
                          int D, RowsOut to, float *dots, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    if (D % V == 0 && wide(x.p, x.ld, sizeof(T)) && (!dots || wide(rows.p, rows.ld, sizeof(T))) &&
-        wide(to.p, to.ld, sizeof(T)))
-        return spread<T, V>(x, at, n_at, w, rows, n, K, D, to, dots, st);
-    return spread<T, 1>(x, at, n_at, w, rows, n, K, D, to, dots, st);
+    int b = min(piece_bytes(x.p, x.ld, D, sizeof(T)), piece_bytes(to.p, to.ld, D, sizeof(T)));
+    if (dots) b = min(b, piece_bytes(rows.p, rows.ld, D, sizeof(T)));
+    return BY_PIECE(T, b, spread, x, at, n_at, w, rows, n, K, D, to, dots, st);
+}
+
+// Positions per chunk: about an expert's average share, so that few experts
+// are cut (a cut costs two partial rows) and few share a warp, between 128
+// (four steps of a warp) and 4096 (an expert with 2^25 pairs then leaves
+// 8192 partial rows).
+uint32_t chunk_of(long long n, int E) {
+    long long c = 128;
+    while (c < 4096 && c < n / E) c <<= 1;
+    return (uint32_t)c;
+}
+
+template <typename T, int VEC>
+cudaError_t segments(RowsIn g, const float *w, const int32_t *offsets, const int32_t *order, long long n, int K,
+                     int E, int D, float *dF, float *partial, cudaStream_t st) {
+    const uint32_t C = chunk_of(n, E), chunks = (uint32_t)((n + C - 1) / C);
+    const dim3 grid((chunks + WARPS - 1) / WARPS, (unsigned)min((D + 32 * VEC - 1) / (32 * VEC), 65535));
+    segment_kernel<T, VEC><<<grid, THREADS, 0, st>>>(static_cast<const T *>(g.p), g.ld, w, offsets, order,
+                                                     (uint32_t)n, K, E, D, group_log(D, VEC), C, chunks, dF, partial);
+    if (chunks > 1) join_kernel<<<chunks - 1, THREADS, 0, st>>>(offsets, (uint32_t)n, E, D, C, partial, dF);
+    return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t segments_typed(RowsIn g, const float *w, const int32_t *offsets, const int32_t *order, long long n_rows,
-                           int K, int E, int D, float *dF, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    const T *p = static_cast<const T *>(g.p);
-    const uint32_t n = (uint32_t)(n_rows * K);
-    if (D % V == 0 && wide(g.p, g.ld, sizeof(T)))
-        segment_kernel<T, V><<<warp_blocks(E), THREADS, 0, st>>>(p, g.ld, w, offsets, order, n, K, E, D, dF);
-    else
-        segment_kernel<T, 1><<<warp_blocks(E), THREADS, 0, st>>>(p, g.ld, w, offsets, order, n, K, E, D, dF);
-    return cudaGetLastError();
+cudaError_t segments_typed(RowsIn g, const float *w, const int32_t *offsets, const int32_t *order, long long n,
+                           int K, int E, int D, float *dF, float *partial, cudaStream_t st) {
+    return BY_PIECE(T, piece_bytes(g.p, g.ld, D, sizeof(T)), segments, g, w, offsets, order, n, K, E, D, dF, partial,
+                    st);
 }
 
 }  // namespace
@@ -230,16 +523,21 @@ cudaError_t launch_spread(int dtype, RowsIn x, const int32_t *at, long long n_at
 }
 
 size_t segment_workspace_bytes(long long n_rows, int K, int E, int D) {
-    (void)n_rows, (void)K, (void)E, (void)D;
-    return 0;
+    const long long n = n_rows * K;
+    const uint32_t C = chunk_of(n, E);
+    return sizeof(float) * 2 * (size_t)((n + C - 1) / C) * D;
 }
 
 cudaError_t launch_segment_sums(int dtype, RowsIn dout, const float *w, const int32_t *offsets, const int32_t *order,
                                 long long T, int K, int E, int D, float *dF, void *ws, cudaStream_t st) {
-    (void)ws;
-    if (dtype == 0) return segments_typed<float>(dout, w, offsets, order, T, K, E, D, dF, st);
-    if (dtype == 1) return segments_typed<__nv_bfloat16>(dout, w, offsets, order, T, K, E, D, dF, st);
-    return segments_typed<__half>(dout, w, offsets, order, T, K, E, D, dF, st);
+    // experts without pairs
+    const cudaError_t e = cudaMemsetAsync(dF, 0, sizeof(float) * (size_t)E * D, st);
+    if (e != cudaSuccess) return e;
+    float *p = static_cast<float *>(ws);
+    const long long n = T * K;
+    if (dtype == 0) return segments_typed<float>(dout, w, offsets, order, n, K, E, D, dF, p, st);
+    if (dtype == 1) return segments_typed<__nv_bfloat16>(dout, w, offsets, order, n, K, E, D, dF, p, st);
+    return segments_typed<__half>(dout, w, offsets, order, n, K, E, D, dF, p, st);
 }
 
 }  // namespace sad
