@@ -519,7 +519,8 @@ int sad_backward_noalloc(int H, int W, int N_cap, const float *records, const ui
  * SAD_BF16, SAD_F16) per row, consecutive, with ld elements from one row to
  * the next (ld >= D); other arrays are dense.  Sums, dot products and
  * statistics are float32; a result of a 16-bit type is rounded once, to
- * nearest even.  No float atomics: results are the same bits on every run.
+ * nearest even.  No float atomics: results are the same bits on every run
+ * with the same sizes, types and alignment.
  * All pointers are device memory of the current device, whose stream is
  * given; row matrices are aligned to their element, workspaces to 16 bytes.
  * Outputs must not overlap inputs except where said.  Every call is

@@ -161,8 +161,7 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const T *__restrict__ R
             }
             if (SUM) {
                 Pack<T, VEC> o;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o.set(i, acc[i]);
+                o.set(acc);
                 store_pack<T, VEC>(out + me.t * ldo + c, o);
             }
         }
@@ -193,12 +192,14 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
 #pragma unroll
             for (int k = 0; k < K_MAX; ++k) {
                 if (id[k] >= n_at) continue;
-                Pack<T, VEC> o;
+                float f[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     if (DOT) dot[k] = fmaf(p[k].get(i), x.get(i), dot[k]);
-                    o.set(i, wt[k] * x.get(i));
+                    f[i] = wt[k] * x.get(i);
                 }
+                Pack<T, VEC> o;
+                o.set(f);
                 store_pack<T, VEC>(S + (long long)id[k] * lds + c, o);
             }
         }
@@ -353,13 +354,6 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const int32_t *__restrict
         }
         __syncthreads();
     }
-}
-
-// the largest piece that base, row distance and D allow: 16 bytes, 4 bytes
-// (16-bit types) or one element
-int piece_bytes(const void *p, long long ld, int D, int bytes) {
-    const uintptr_t all = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * bytes) | (uintptr_t)((long long)D * bytes);
-    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : bytes;
 }
 
 int ceil_log2(int v) {

@@ -21,11 +21,47 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
 // VEC consecutive elements as one aligned load or store of VEC * sizeof(T)
-// bytes (at most 16)
-template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack {
+// bytes (at most 16).  Pairs of 16-bit elements stay 32-bit words: taken out
+// one by one and rounded one by one they cost about twice the instructions
+// (25 per element of a layer norm).
+template <typename T, int VEC, bool PAIRS = sizeof(T) == 2 && VEC % 2 == 0> struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
     __device__ __forceinline__ float get(int i) const { return to_f32<T>(v[i]); }
-    __device__ __forceinline__ void set(int i, float f) { v[i] = from_f32<T>(f); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = from_f32<T>(0.0f);
+    }
+    __device__ __forceinline__ void set(const float (&f)[VEC]) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = from_f32<T>(f[i]);
+    }
+};
+__device__ __forceinline__ float half_of(uint32_t w, int i, __nv_bfloat16) {
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+}
+__device__ __forceinline__ float half_of(uint32_t w, int i, __half) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+    return i & 1 ? __high2float(h) : __low2float(h);
+}
+__device__ __forceinline__ uint32_t pair_of(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pair_of(float a, float b, __half) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack<T, VEC, true> {
+    uint32_t w[VEC / 2];
+    __device__ __forceinline__ float get(int i) const { return half_of(w[i / 2], i, T()); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void set(const float (&f)[VEC]) {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) w[i] = pair_of(f[2 * i], f[2 * i + 1], T());
+    }
 };
 
 template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p) {
@@ -41,6 +77,13 @@ template <int L> __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// the largest piece that base, row distance and D allow: 16 bytes, 4 bytes
+// (16-bit types) or one element
+inline int piece_bytes(const void *p, long long ld, int D, int bytes) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * bytes) | (uintptr_t)((long long)D * bytes);
+    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : bytes;
 }
 
 }  // namespace sad

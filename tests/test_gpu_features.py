@@ -252,8 +252,9 @@ def test_layer_norm(T, D, pad, shift, dt, affine):
     close(rstd, rs[:, 0], (erel * rs)[:, 0])
     eh = em * rs + h.abs() * (erel + 2 * U)
     close(y, h * gd + bd, eh * gd.abs() + 3 * U * ((h * gd).abs() + bd.abs()))
-    # in place: the same bits
-    x2 = x.clone()
+    # in place: the same bits (rows laid out alike: sums may be shared out
+    # over the lanes by the rows' alignment)
+    x2 = strided(x, pad, shift)
     y2, _, _ = f.layer_norm(x2, gamma, beta, 1e-3, out=x2)
     assert y2 is x2 and torch.equal(y2, y)
 
@@ -274,10 +275,10 @@ def test_layer_norm(T, D, pad, shift, dt, affine):
     close(dg, (dyd * h).sum(0), (T + 4) * U * (dyd * h).abs().sum(0) + (dyd.abs() * eh).sum(0))
     close(db, dyd.sum(0), (T + 1) * U * dyd.abs().sum(0))
     # dx in the place of dy, sums not wanted, the same bits
-    dy2 = dy.clone()
+    dy2 = strided(dy, pad, shift)
     dx2, n1, n2 = f.layer_norm_backward(dy2, x, gamma, mean, rstd, want_affine=False, dx=dy2)
     assert dx2 is dy2 and n1 is None and n2 is None and torch.equal(dx2, dx)
-    dy2 = dy.clone()
+    dy2 = strided(dy, pad, shift)
     dx3, dg3, db3 = f.layer_norm_backward(dy2, x, gamma, mean, rstd, dx=dy2)
     assert torch.equal(dx3, dx) and torch.equal(dg3, dg) and torch.equal(db3, db)
 
@@ -382,7 +383,7 @@ def test_distill(T, V, M, pad, shift, dt, tau):
     # loss alone, and the gradient in the logits' place: the same bits
     alone, none = f.distill(z, tid, tl, tau, rw, want_grad=False)
     assert none is None and torch.equal(alone, loss)
-    z2 = z.clone()
+    z2 = strided(z, pad, shift)
     _, same = f.distill(z2, tid, tl, tau, rw, dlogits=z2)
     assert same is z2 and torch.equal(same, dz)
     ones, dz1 = f.distill(z, tid, tl, tau)
