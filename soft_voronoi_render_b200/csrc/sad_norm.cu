@@ -203,9 +203,8 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : THREADS, BLOCK ? 1 : 2) norm_b
                     dg[k] = fmaf(dk, hk, dg[k]);
                     db[k] += dk;
                 }
-                const float gk = dk * gm[q];
-                a += gk;
-                b = fmaf(gk, hk, b);
+                a = fmaf(dk, gm[q], a);
+                b = fmaf(__fmul_rn(dk, gm[q]), hk, b);
             }
         }
         if (BLOCK) {
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : THREADS, BLOCK ? 1 : 2) norm_b
 #pragma unroll
             for (int q = 0; q < VEC; ++q) {
                 const float hk = (h.p[i].get(q) - m) * rs;
-                f[q] = rs * (g.p[i].get(q) * gm[q] - fmaf(hk, b, a));
+                f[q] = rs * fmaf(g.p[i].get(q), gm[q], -fmaf(hk, b, a));
             }
             Pack<T, VEC> o;
             o.set(f);
@@ -330,22 +329,42 @@ template <typename T, int NV, int ROWS> struct Ring {
     __device__ __forceinline__ void next() { slot = slot + 1 == STAGES ? 0 : slot + 1; }
 };
 
-// sums of `mine` over the warps of the block for each of ROWS rows, the same
+// The backward kernels write out which products are fused with which sums, so
+// that dx has the same bits with and without the sums.
+
+// sums of `mine` over the warps of the block for each of N values, the same
 // bits in every thread; one barrier
-template <int ROWS>
-__device__ __forceinline__ void block_sums(const float (&mine)[ROWS], float (*scratch)[32], float (&all)[ROWS]) {
+template <int N>
+__device__ __forceinline__ void block_sums(const float (&mine)[N], float (*scratch)[32], float (&all)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float s[N];
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-        const float s = group_sum<32>(mine[j]);
-        if (lane == 0) scratch[j][warp] = s;
+    for (int j = 0; j < N; ++j) s[j] = mine[j];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) scratch[j][warp] = s[j];
     }
     __syncthreads();
+    // at most 16 warps
 #pragma unroll
-    for (int j = 0; j < ROWS; ++j) all[j] = group_sum<32>(lane < warps ? scratch[j][lane] : 0.0f);
+    for (int j = 0; j < N; ++j) s[j] = (lane & 15) < warps ? scratch[j][lane & 15] : 0.0f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) all[j] = s[j];
 }
 
-// ROWS rows a block, side by side
+// ROWS rows a block, side by side.  Only a thread's last piece may lie beyond
+// the row (wide_threads), and nothing branches on it but loads and stores: with
+// branches between the pieces the loads of one waited for the sums of another.
 template <typename T, int NV, int ROWS>
 __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, long long ldx,
                                                                     const float *__restrict__ gamma,
@@ -378,10 +397,10 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, 
         s[j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (c0 + i * step >= D) break;
+            const bool in = i < NV - 1 || c0 + i * step < D;
 #pragma unroll
             for (int q = 0; q < VEC; ++q) {
-                const float d = row[j].p[i].get(q) - m[j];
+                const float d = in ? row[j].p[i].get(q) - m[j] : 0.0f;
                 s[j] = fmaf(d, d, s[j]);
             }
         }
@@ -394,20 +413,19 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, 
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = c0 + i * step;
-        if (c >= D) break;
+        const int c = min(c0 + i * step, D - VEC);
+        const bool in = i < NV - 1 || c0 + i * step < D;
         float g[VEC], b[VEC];
         load_param<VEC>(gamma, c, 1.0f, g);
         load_param<VEC>(beta, c, 0.0f, b);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            if (r0 + j >= n) break;
             float f[VEC];
 #pragma unroll
             for (int q = 0; q < VEC; ++q) f[q] = fmaf((row[j].p[i].get(q) - m[j]) * rs[j], g[q], b[q]);
             Pack<T, VEC> o;
             o.set(f);
-            store_pack<T, VEC>(y + (r0 + j) * ldy + c, o);
+            if (in && r0 + j < n) store_pack<T, VEC>(y + (r0 + j) * ldy + c, o);
         }
     }
     if (threadIdx.x < ROWS && r0 + threadIdx.x < n) {
@@ -458,7 +476,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
     for (int s = 0; s < R::STAGES - 1; ++s) fetch(s, r + s * stride);
     fetch_stats(r);
     for (int turn = 0; r < n; r += stride, turn ^= 1) {
-        fetch((ring.slot + R::STAGES - 1) % R::STAGES, r + (R::STAGES - 1) * stride);
+        fetch(ring.slot ? ring.slot - 1 : R::STAGES - 1, r + (R::STAGES - 1) * stride);
         float m[ROWS], rs[ROWS], sums[2 * ROWS], all[2 * ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) m[j] = m_next[j], rs[j] = rs_next[j];
@@ -469,15 +487,18 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
         for (int j = 0; j < 2 * ROWS; ++j) sums[j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
-            if (c >= pieces) break;
+            const int c = min(i * (int)blockDim.x + (int)threadIdx.x, pieces - 1);
+            const bool in = i < NV - 1 || i * (int)blockDim.x + (int)threadIdx.x < pieces;
             float gm[VEC];
             load_param<VEC>(gamma, c * VEC, 1.0f, gm);
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
-                if (r + j >= n) break;
-                g[j].p[i] = ring.get(2 * j, i);
-                h[j].p[i] = ring.get(2 * j + 1, i);
+                g[j].p[i].clear();
+                h[j].p[i].clear();
+                if (in && r + j < n) {
+                    g[j].p[i] = ring.get(2 * j, i);
+                    h[j].p[i] = ring.get(2 * j + 1, i);
+                }
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) {
                     const int k = i * VEC + q;
@@ -486,9 +507,8 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
                         dg[k] = fmaf(dk, hk, dg[k]);
                         db[k] += dk;
                     }
-                    const float gk = dk * gm[q];
-                    sums[2 * j] += gk;
-                    sums[2 * j + 1] = fmaf(gk, hk, sums[2 * j + 1]);
+                    sums[2 * j] = fmaf(dk, gm[q], sums[2 * j]);
+                    sums[2 * j + 1] = fmaf(__fmul_rn(dk, gm[q]), hk, sums[2 * j + 1]);
                 }
             }
         }
@@ -502,23 +522,22 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
-            if (c >= pieces) break;
+            const int c = min(i * (int)blockDim.x + (int)threadIdx.x, pieces - 1);
+            const bool in = i < NV - 1 || i * (int)blockDim.x + (int)threadIdx.x < pieces;
             float gm[VEC];
             load_param<VEC>(gamma, c * VEC, 1.0f, gm);
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
-                if (r + j >= n) break;
                 const float a = all[2 * j] * inv, b = all[2 * j + 1] * inv;
                 float f[VEC];
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) {
                     const float hk = (h[j].p[i].get(q) - m[j]) * rs[j];
-                    f[q] = rs[j] * (g[j].p[i].get(q) * gm[q] - fmaf(hk, b, a));
+                    f[q] = rs[j] * fmaf(g[j].p[i].get(q), gm[q], -fmaf(hk, b, a));
                 }
                 Pack<T, VEC> o;
                 o.set(f);
-                store_pack<T, VEC>(dx + (r + j) * lddx + (long long)c * VEC, o);
+                if (in && r + j < n) store_pack<T, VEC>(dx + (r + j) * lddx + (long long)c * VEC, o);
             }
         }
     }
@@ -626,6 +645,7 @@ int wide_pieces(int pieces) {
 // rows side by side: a second one hides the first one's reductions, where the
 // registers of its pieces are there
 constexpr int wide_rows(int nv) { return nv == 2 ? 2 : 1; }
+// (fewer pieces than nv * threads, never fewer than (nv - 1) * threads)
 int wide_threads(int pieces, int nv) { return ((pieces + nv - 1) / nv + 31) / 32 * 32; }
 
 template <typename F> cudaError_t allow_shared(F kernel, size_t bytes) {
