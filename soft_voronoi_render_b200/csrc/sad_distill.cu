@@ -8,15 +8,18 @@
 // of z log2(e) / tau, about the row's maximum, in float32.
 //
 // Bound by memory where rows are read and written once; the exponentials (16
-// a clock on a multiprocessor) come next.  Short rows (up to 8 pieces of at
-// most 16 bytes for each lane of a group of L <= 32) stay in registers,
-// several rows a warp.  Longer rows are shared by a block, which keeps its
-// part in shared memory from the first pass (running maximum and sum of every
-// thread) to the second (gradient); a row beyond 100 KB, or one of few rows,
-// by a cluster of up to eight blocks that join maxima and sums through
-// distributed shared memory.  Rows start at any element: the pieces begin at
-// the row's first 16-byte boundary, and the elements before and behind them
-// are taken one by one.
+// a clock on a multiprocessor, two an element with the gradient of a long
+// row) come next.  Rows start at any element: the 16-byte pieces begin at the
+// row's first boundary, and the elements before and behind them, its edges,
+// are taken one by one.  Short rows (up to 8 pieces for each lane of a group
+// of L <= 32) stay in registers, several rows a warp.  Longer rows are shared
+// by a block, which keeps its part in shared memory from the first pass
+// (running maximum and sum of every thread) to the second (gradient); a row
+// beyond 100 KB, or one of few rows, by a cluster of up to eight blocks that
+// join maxima and sums through distributed shared memory.
+#include <algorithm>
+#include <type_traits>
+
 #include <cooperative_groups.h>
 
 #include "sad_features.h"
@@ -27,6 +30,8 @@ namespace sad {
 namespace {
 
 namespace cg = cooperative_groups;
+using std::max;
+using std::min;
 
 constexpr int SMS = 148;
 constexpr int M_MAX = 128;
@@ -133,27 +138,118 @@ __device__ __forceinline__ float teacher_grad(const Teacher &t, int M, int m, fl
     return scale * (exp2_fast(t.zid[m] - big) * inv_sum - q);
 }
 
+// the largest of a piece's elements and m, as loaded; 16-bit ones in pairs
+template <typename T, int VEC> __device__ __forceinline__ float piece_max(const Pack<T, VEC> &p, float m) {
+    if constexpr (sizeof(T) == 2 && VEC == 8) {
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        T2 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const T2 *>(&p.w[i]);
+        const T2 a = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+        return max_nan(m, max_nan(to_f32<T>(a.x), to_f32<T>(a.y)));
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) m = max_nan(m, p.get(q));
+        return m;
+    }
+}
+
+// e = 2^(z k - big) of a piece
+template <typename T, int VEC>
+__device__ __forceinline__ void piece_exp(const Pack<T, VEC> &p, float k, float big, float (&e)[VEC]) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 2) {
+            both(fma_two(two(p.get(q), p.get(q + 1)), two(k, k), two(-big, -big)), e[q], e[q + 1]);
+            e[q] = exp2_fast(e[q]);
+            e[q + 1] = exp2_fast(e[q + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) e[q] = exp2_fast(fmaf(p.get(q), k, -big));
+    }
+}
+
+// s += the elements of e
+template <int VEC> __device__ __forceinline__ void piece_add(const float (&e)[VEC], Two &s) {
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 2) s = add_two(s, two(e[q], e[q + 1]));
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) s = add_two(s, two(e[q], 0.0f));
+    }
+}
+
+// to[] = e f, as one piece where `to` is on a boundary
+template <typename T, int VEC>
+__device__ __forceinline__ void store_scaled(T *to, const float (&e)[VEC], float f, bool whole) {
+    float g[VEC];
+    if constexpr (VEC % 2 == 0) {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 2) both(mul_two(two(e[q], e[q + 1]), two(f, f)), g[q], g[q + 1]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) g[q] = e[q] * f;
+    }
+    if (whole) {
+        Pack<T, VEC> o;
+        o.set(g);
+        store_pack<T, VEC>(to, o);
+    } else {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) to[q] = from_f32<T>(g[q]);
+    }
+}
+
+// Where a row's pieces of VEC elements lie: `head` elements before the first,
+// `pieces` of them, `tail` elements behind
+template <typename T, int VEC> struct Cut {
+    int head, pieces, tail;
+    __device__ __forceinline__ Cut(const T *row, int V, bool edges) {
+        head = edges ? min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T))) : 0;
+        pieces = (V - head) / VEC;
+        tail = V - head - pieces * VEC;
+    }
+    // the q-th of the row's elements outside the pieces, V if there are fewer
+    __device__ __forceinline__ int edge(int q, int V) const {
+        return q < head ? q : q < head + tail ? V - tail + q - head : V;
+    }
+    // the piece of element id, -1 for an edge
+    __device__ __forceinline__ int piece_of(int id, int V) const {
+        return id < head || id >= V - tail ? -1 : (id - head) / VEC;
+    }
+};
+
+__device__ __forceinline__ bool same_boundaries(const void *a, const void *b) {
+    return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+}
+
 // ---------------------------------------------------------------------------
 // short rows
 // ---------------------------------------------------------------------------
 constexpr int GROUP_THREADS = 256;
 
-template <typename T, int VEC, int NV, bool GRAD>
+template <typename T, int VEC, int NV, bool EDGES, bool GRAD>
 __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     const T *z, long long ldz, const int32_t *__restrict__ tid, const float *__restrict__ tl,
     const float *__restrict__ rw, long long n, int V, int M, float tau, int log_l, float *__restrict__ loss, T *dz,
     long long lddz) {
     extern __shared__ float teacher_space[];
     const int L = 1 << log_l, lane = threadIdx.x & (L - 1), group = threadIdx.x >> log_l;
-    const int c0 = lane * VEC, step = L * VEC;
     const long long t = ((long long)blockIdx.x * GROUP_THREADS + threadIdx.x) >> log_l;
     const bool in = t < n;
     const float k = LOG2E / tau;
     const T *row = z + t * ldz;
+    const Cut<T, VEC> cut(row, V, EDGES);
+    const int pieces = in ? cut.pieces : 0;
     Pack<T, VEC> p[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (in && c0 + i * step < V) p[i] = load_pack<T, VEC>(row + c0 + i * step);
+        if (lane + i * L < pieces) p[i] = load_pack<T, VEC>(row + cut.head + (lane + i * L) * VEC);
+    const int edge = EDGES && in ? cut.edge(lane, V) : V;
+    float edge_z = minus_infinity();
+    if (EDGES && edge < V) edge_z = to_f32<T>(row[edge]);
     const float weight = in ? (rw ? __ldg(rw + t) : 1.0f) : 0.0f;
     Teacher te;
     float *space = teacher_space + (size_t)group * M * 3;
@@ -163,42 +259,42 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, k, in, lane, L);
     teacher_softmax(te, M, lane, L);
 
-    float e[NV * VEC];
-    float big = minus_infinity();
+    float big = EDGES ? edge_z : minus_infinity();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (lane + i * L < pieces) big = piece_max(p[i], big);
+    big = lanes_max(big, L) * k;
+    const bool live = te.any && weight != 0.0f && big != minus_infinity();
+    if (!live) {  // the row may hold anything: take 0 for it
+#pragma unroll
+        for (int i = 0; i < NV; ++i) p[i].clear();
+        edge_z = 0.0f;
+        big = 0.0f;
+    }
+    float e[NV][VEC];
+    Two sums = two(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const bool on = in && c0 + i * step < V;
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-            e[i * VEC + q] = on ? p[i].get(q) * k : minus_infinity();
-            big = max_nan(big, e[i * VEC + q]);
+        if (lane + i * L < pieces) {
+            piece_exp(p[i], k, big, e[i]);
+            piece_add(e[i], sums);
         }
     }
-    big = lanes_max(big, L);
-    const bool live = te.any && weight != 0.0f && big != minus_infinity();
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV * VEC; ++i) {
-        e[i] = exp2_fast(e[i] - big);
-        sum += e[i];
-    }
-    sum = lanes_sum(sum, L);
+    float sum, other;
+    both(sums, sum, other);
+    sum += other;
+    const float edge_e = EDGES && edge < V ? exp2_fast(fmaf(edge_z, k, -big)) : 0.0f;
+    sum = lanes_sum(sum + edge_e, L);
     const float part = teacher_loss(te, M, lane, L, big, sum);
     if (lane == 0 && in) loss[t] = live ? weight * tau * tau * part : 0.0f;
     if (!GRAD) return;
-    const float scale = weight * tau, is = 1.0f / sum, f = scale * is;
+    const float scale = weight * tau, is = 1.0f / sum, f = live ? scale * is : 0.0f;
     T *out = dz + t * lddz;
+    const bool whole = !EDGES || same_boundaries(out, row);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = c0 + i * step;
-        if (!in || c >= V) continue;
-        float g[VEC];
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) g[q] = live ? e[i * VEC + q] * f : 0.0f;
-        Pack<T, VEC> o;
-        o.set(g);
-        store_pack<T, VEC>(out + c, o);
-    }
+    for (int i = 0; i < NV; ++i)
+        if (lane + i * L < pieces) store_scaled(out + cut.head + (lane + i * L) * VEC, e[i], f, whole);
+    if (EDGES && edge < V) out[edge] = from_f32<T>(edge_e * f);
     __syncwarp();
     // the teacher's classes once more, from float32: an id listed twice gets
     // the same value from each of its entries
@@ -213,7 +309,7 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
 constexpr int LONG_THREADS = 512;
 
 template <typename T, bool GRAD, bool CACHE>
-__global__ void __launch_bounds__(LONG_THREADS) distill_long_kernel(
+__global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
     const T *z, long long ldz, const int32_t *__restrict__ tid, const float *__restrict__ tl,
     const float *__restrict__ rw, int V, int M, float tau, int each, float *__restrict__ loss, T *dz,
     long long lddz) {
@@ -225,17 +321,14 @@ __global__ void __launch_bounds__(LONG_THREADS) distill_long_kernel(
     __shared__ float block_max, block_sum, t_any;
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, B = blockDim.x;
     const long long t = blockIdx.x / ranks;
     const T *row = z + t * ldz;
     const float k = LOG2E / tau;
     const float weight = rw ? __ldg(rw + t) : 1.0f;
-
-    // elements before the first 16-byte boundary, whole pieces, elements behind
-    const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T)));
-    const int pieces = (V - head) / VEC, tail = V - head - pieces * VEC;
-    const int first = min(rank * each, pieces), last = min(first + each, pieces);
-    const uint4 *body = reinterpret_cast<const uint4 *>(row + head);
+    const Cut<T, VEC> cut(row, V, true);
+    const int first = min(rank * each, cut.pieces), last = min(first + each, cut.pieces);
+    const T *body = row + cut.head;
 
     Teacher te{s_id, s_q, s_zid, 0.0f, 0.0f, false};
     if (warp == 0) {
@@ -244,60 +337,57 @@ __global__ void __launch_bounds__(LONG_THREADS) distill_long_kernel(
         if (lane == 0) t_any = te.any ? 1.0f : 0.0f;
     }
 
-    // each thread's running maximum and sum of exponentials about it
+    // each thread's running maximum (as loaded) and sum of exponentials about
+    // it; one thread of the first block takes an edge each
+    const int edge = rank ? V : cut.edge(threadIdx.x, V);
     float big = minus_infinity(), sum = 0.0f;
-    auto take = [&](const float *a, int count) {
-        float m = big;
-        for (int i = 0; i < count; ++i) m = max_nan(m, a[i]);
-        const float m0 = finite_max(m);
-        sum *= exp2_fast(big - m0);  // big = -inf: sum is 0
-        for (int i = 0; i < count; ++i) sum += exp2_fast(a[i] - m0);
-        big = m;
-    };
-    // one of the elements outside the pieces, for one thread of the first block
-    const int edge = rank ? V : (int)threadIdx.x < head ? (int)threadIdx.x
-                              : (int)threadIdx.x < head + tail ? V - tail + (int)threadIdx.x - head : V;
-    float edge_z = 0.0f;
     if (edge < V) {
-        edge_z = to_f32<T>(row[edge]) * k;
-        take(&edge_z, 1);
+        big = to_f32<T>(row[edge]);
+        sum = big == minus_infinity() ? 0.0f : exp2_fast(fmaf(big, k, -big * k));
     }
-    for (int c = first + threadIdx.x; c < last; c += UNROLL * blockDim.x) {
+    const float edge_z = big;
+    for (int c = first + threadIdx.x; c < last; c += UNROLL * B) {
         Pack<T, VEC> p[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-            if (c + u * (int)blockDim.x < last)
-                p[u] = load_pack<T, VEC>(reinterpret_cast<const T *>(body + c + u * blockDim.x));
-        float a[UNROLL * VEC];
+        float m = big;
+        // whole steps, and the last one, whose missing pieces repeat the first
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const bool on = c + u * (int)blockDim.x < last;
-            if (GRAD && CACHE && on) cache[c + u * blockDim.x - first] = *reinterpret_cast<const uint4 *>(&p[u]);
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) a[u * VEC + q] = on ? p[u].get(q) * k : minus_infinity();
+            const int at = c + u * B;
+            p[u] = load_pack<T, VEC>(body + (long long)(at < last ? at : c) * VEC);
         }
-        float m = big;
 #pragma unroll
-        for (int i = 0; i < UNROLL * VEC; ++i) m = max_nan(m, a[i]);
-        const float m0 = finite_max(m);
-        float s = 0.0f;
+        for (int u = 0; u < UNROLL; ++u) {
+            const int at = c + u * B;
+            if (GRAD && CACHE && at < last) cache[at - first] = *reinterpret_cast<const uint4 *>(&p[u]);
+            m = piece_max(p[u], m);
+        }
+        const float m0 = finite_max(m) * k;
+        Two s = two(sum * exp2_fast(big == minus_infinity() ? big : fmaf(big, k, -m0)), 0.0f);
 #pragma unroll
-        for (int i = 0; i < UNROLL * VEC; ++i) s += exp2_fast(a[i] - m0);
-        sum = fmaf(sum, exp2_fast(big - m0), s);
+        for (int u = 0; u < UNROLL; ++u) {
+            if (c + u * B < last) {
+                float e[VEC];
+                piece_exp(p[u], k, m0, e);
+                piece_add(e, s);
+            }
+        }
+        float other;
+        both(s, sum, other);
+        sum += other;
         big = m;
     }
 
     // joined over the warps, then over the cluster
     {
         const float m = lanes_max(big, 32);
-        const float s = lanes_sum(sum * exp2_fast(big - finite_max(m)), 32);
+        const float s = lanes_sum(big == minus_infinity() ? 0.0f : sum * exp2_fast((big - finite_max(m)) * k), 32);
         if (lane == 0) s_max[warp] = m, s_sum[warp] = s;
     }
     __syncthreads();
     {
         const float wm = lane < warps ? s_max[lane] : minus_infinity(), ws = lane < warps ? s_sum[lane] : 0.0f;
         big = lanes_max(wm, 32);
-        sum = lanes_sum(ws * exp2_fast(wm - finite_max(big)), 32);
+        sum = lanes_sum(wm == minus_infinity() ? 0.0f : ws * exp2_fast((wm - finite_max(big)) * k), 32);
     }
     if (ranks > 1) {
         if (threadIdx.x == 0) block_max = big, block_sum = sum;
@@ -305,9 +395,10 @@ __global__ void __launch_bounds__(LONG_THREADS) distill_long_kernel(
         const float wm = lane < ranks ? *cluster.map_shared_rank(&block_max, lane) : minus_infinity();
         const float ws = lane < ranks ? *cluster.map_shared_rank(&block_sum, lane) : 0.0f;
         big = lanes_max(wm, 32);
-        sum = lanes_sum(ws * exp2_fast(wm - finite_max(big)), 32);
-        cluster.sync();  // no block leaves, or writes a class that another still reads, before all have read
+        sum = lanes_sum(wm == minus_infinity() ? 0.0f : ws * exp2_fast((wm - finite_max(big)) * k), 32);
+        cluster.sync();  // no block leaves before all have read its shared memory
     }
+    big *= k;
     const bool live = t_any != 0.0f && weight != 0.0f && big != minus_infinity();
     if (warp == 0) {
         const float part = teacher_loss(te, M, lane, 32, big, sum);
@@ -315,50 +406,43 @@ __global__ void __launch_bounds__(LONG_THREADS) distill_long_kernel(
     }
     if (!GRAD) return;
     const float scale = weight * tau, is = 1.0f / sum, f = scale * is;
-    T *out = dz + t * lddz;
-    const bool same_phase = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
-    if (edge < V) out[edge] = from_f32<T>(live ? exp2_fast(edge_z - big) * f : 0.0f);
-    for (int c = first + threadIdx.x; c < last; c += UNROLL * blockDim.x) {
-        Pack<T, VEC> p[UNROLL];
+    T *out = dz + t * lddz, *out_body = out + cut.head;
+    const bool whole = same_boundaries(out, row);
+    if (edge < V) out[edge] = from_f32<T>(live ? exp2_fast(fmaf(edge_z, k, -big)) * f : 0.0f);
+    if (live) {
+        for (int c = first + threadIdx.x; c < last; c += UNROLL * B) {
+            Pack<T, VEC> p[UNROLL];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int at = c + u * (int)blockDim.x;
-            if (at < last)
-                p[u] = load_pack<T, VEC>(reinterpret_cast<const T *>(CACHE ? cache + at - first : body + at));
-        }
+            for (int u = 0; u < UNROLL; ++u) {
+                const int at = c + u * B < last ? c + u * B : c;
+                if (CACHE) p[u] = *reinterpret_cast<const Pack<T, VEC> *>(cache + at - first);
+                else p[u] = load_pack<T, VEC>(body + (long long)at * VEC);
+            }
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int at = c + u * (int)blockDim.x;
-            if (at >= last) continue;
-            float g[VEC];
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) g[q] = live ? exp2_fast(fmaf(p[u].get(q), k, -big)) * f : 0.0f;
-            T *to = out + head + (long long)at * VEC;
-            if (same_phase) {
-                Pack<T, VEC> o;
-                o.set(g);
-                store_pack<T, VEC>(to, o);
-            } else {
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) to[q] = from_f32<T>(g[q]);
+            for (int u = 0; u < UNROLL; ++u) {
+                const int at = c + u * B;
+                float e[VEC];
+                piece_exp(p[u], k, big, e);
+                if (at < last) store_scaled(out_body + (long long)at * VEC, e, f, whole);
             }
         }
+    } else {
+        const float zero[VEC] = {};
+        for (int c = first + threadIdx.x; c < last; c += B) store_scaled(out_body + (long long)c * VEC, zero, 0.0f, whole);
     }
     __syncthreads();
     // the teacher's classes in this block's part, from float32
-    if (live && threadIdx.x < M && s_id[threadIdx.x] >= 0) {
-        const int id = s_id[threadIdx.x];
-        const int piece = id < head || id >= V - tail ? -1 : (id - head) / VEC;
-        if (piece < 0 ? rank == 0 : (piece >= first && piece < last))
-            out[id] = from_f32<T>(teacher_grad(te, M, threadIdx.x, big, is, scale));
-    }
+    if (live)
+        for (int m = threadIdx.x; m < M; m += B) {
+            if (s_id[m] < 0) continue;
+            const int piece = cut.piece_of(s_id[m], V);
+            if (piece < 0 ? rank == 0 : (piece >= first && piece < last))
+                out[s_id[m]] = from_f32<T>(teacher_grad(te, M, m, big, is, scale));
+        }
 }
 
-// the piece that a row at any of the n row starts can be read in
-int row_piece(const void *p, long long ld, int V, int bytes) {
-    const uintptr_t all = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * bytes) | (uintptr_t)((long long)V * bytes);
-    return (all & 15) == 0 ? 16 : (all & 7) == 0 ? 8 : (all & 3) == 0 ? 4 : bytes;
-}
+// whether every row begins and ends on a 16-byte boundary
+bool whole_rows(const void *p, long long ld, int V, int bytes) { return piece_bytes(p, ld, V, bytes) == 16; }
 
 struct Args {
     const int32_t *tid;
@@ -369,7 +453,7 @@ struct Args {
     float *loss;
 };
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, bool EDGES>
 cudaError_t group_launch(RowsIn z, RowsOut dz, const Args &a, int log_l, cudaStream_t st) {
     const int groups = GROUP_THREADS >> log_l;
     const unsigned blocks = (unsigned)((a.n + groups - 1) / groups);
@@ -377,33 +461,39 @@ cudaError_t group_launch(RowsIn z, RowsOut dz, const Args &a, int log_l, cudaStr
     const T *zp = static_cast<const T *>(z.p);
     T *dzp = static_cast<T *>(dz.p);
     if (dzp)
-        distill_group_kernel<T, VEC, NV, true><<<blocks, GROUP_THREADS, shared, st>>>(
+        distill_group_kernel<T, VEC, NV, EDGES, true><<<blocks, GROUP_THREADS, shared, st>>>(
             zp, z.ld, a.tid, a.tl, a.rw, a.n, a.V, a.M, a.tau, log_l, a.loss, dzp, dz.ld);
     else
-        distill_group_kernel<T, VEC, NV, false><<<blocks, GROUP_THREADS, shared, st>>>(
+        distill_group_kernel<T, VEC, NV, EDGES, false><<<blocks, GROUP_THREADS, shared, st>>>(
             zp, z.ld, a.tid, a.tl, a.rw, a.n, a.V, a.M, a.tau, log_l, a.loss, dzp, dz.ld);
     return cudaGetLastError();
 }
 
 constexpr int GROUP_PIECES = 8;  // a lane, at most
 
-template <typename T, int VEC> cudaError_t group_shape(RowsIn z, RowsOut dz, const Args &a, cudaStream_t st) {
-    const int pieces = (a.V + VEC - 1) / VEC;
+template <typename T, int VEC, bool EDGES> cudaError_t group_shape(RowsIn z, RowsOut dz, const Args &a, cudaStream_t st) {
+    const int pieces = EDGES ? max(1, a.V / VEC) : (a.V + VEC - 1) / VEC;
     // the lanes that leave the fewest idle, the fewest on a tie; enough of
-    // them that the groups' teachers fit 48 KB
+    // them for every edge, and that the groups' teachers fit 48 KB
+    const int least = EDGES ? 2 * (VEC - 1) : 1;
     int log_l = 5, best = 1 << 30;
     for (int l = 0; l <= 5; ++l) {
         const int each = (pieces + (1 << l) - 1) >> l;
-        if (each > GROUP_PIECES || (GROUP_THREADS >> l) * a.M * 12 > 48 * 1024) continue;
+        if ((1 << l) < least || each > GROUP_PIECES || (GROUP_THREADS >> l) * a.M * 12 > 48 * 1024) continue;
         if ((each << l) < best) {
             best = each << l;
             log_l = l;
         }
     }
-    const int each = (pieces + (1 << log_l) - 1) >> log_l;
-    return each <= 2   ? group_launch<T, VEC, 2>(z, dz, a, log_l, st)
-           : each <= 4 ? group_launch<T, VEC, 4>(z, dz, a, log_l, st)
-                       : group_launch<T, VEC, GROUP_PIECES>(z, dz, a, log_l, st);
+    switch ((pieces + (1 << log_l) - 1) >> log_l) {
+        case 1: return group_launch<T, VEC, 1, EDGES>(z, dz, a, log_l, st);
+        case 2: return group_launch<T, VEC, 2, EDGES>(z, dz, a, log_l, st);
+        case 3: return group_launch<T, VEC, 3, EDGES>(z, dz, a, log_l, st);
+        case 4: return group_launch<T, VEC, 4, EDGES>(z, dz, a, log_l, st);
+        case 5: return group_launch<T, VEC, 5, EDGES>(z, dz, a, log_l, st);
+        case 6: return group_launch<T, VEC, 6, EDGES>(z, dz, a, log_l, st);
+        default: return group_launch<T, VEC, GROUP_PIECES, EDGES>(z, dz, a, log_l, st);
+    }
 }
 
 template <typename T> cudaError_t long_launch(RowsIn z, RowsOut dz, const Args &a, cudaStream_t st) {
@@ -417,7 +507,9 @@ template <typename T> cudaError_t long_launch(RowsIn z, RowsOut dz, const Args &
         ranks *= 2;
     const int each = (pieces + ranks - 1) / ranks;
     const bool cached = each <= MOST;
-    const int threads = each <= 256 ? 128 : each <= 1024 ? 256 : LONG_THREADS;
+    // about eight pieces a thread: with more threads a block of short rows
+    // waits for its reductions most of the time
+    const int threads = each <= 1024 ? 128 : each <= 2048 ? 256 : LONG_THREADS;
     const size_t shared = dz.p && cached ? (size_t)each * 16 : 0;
     auto kernel = !dz.p ? distill_long_kernel<T, false, true>
                         : cached ? distill_long_kernel<T, true, true> : distill_long_kernel<T, true, false>;
@@ -446,13 +538,14 @@ template <typename T> cudaError_t long_launch(RowsIn z, RowsOut dz, const Args &
 }
 
 template <typename T> cudaError_t distill(RowsIn z, RowsOut dz, const Args &a, cudaStream_t st) {
-    int b = row_piece(z.p, z.ld, a.V, sizeof(T));
-    if (dz.p) b = b < row_piece(dz.p, dz.ld, a.V, sizeof(T)) ? b : row_piece(dz.p, dz.ld, a.V, sizeof(T));
-    if ((long long)a.V * (int)sizeof(T) > 32ll * GROUP_PIECES * b) return long_launch<T>(z, dz, a, st);
-    if (b == 16) return group_shape<T, 16 / sizeof(T)>(z, dz, a, st);
-    if (b == 8) return group_shape<T, 8 / sizeof(T)>(z, dz, a, st);
-    if (b == 4) return group_shape<T, 4 / sizeof(T)>(z, dz, a, st);
-    return group_shape<T, 1>(z, dz, a, st);
+    constexpr int VEC = 16 / sizeof(T);
+    if (a.V > 32 * GROUP_PIECES * VEC) return long_launch<T>(z, dz, a, st);
+    const bool whole = whole_rows(z.p, z.ld, a.V, sizeof(T)) && (!dz.p || whole_rows(dz.p, dz.ld, a.V, sizeof(T)));
+    if (whole) return group_shape<T, VEC, false>(z, dz, a, st);
+    // in pieces with edges, but element by element where the edges' lanes
+    // would outnumber the pieces
+    if (a.V > 8 * VEC) return group_shape<T, VEC, true>(z, dz, a, st);
+    return group_shape<T, 1, false>(z, dz, a, st);
 }
 
 }  // namespace
