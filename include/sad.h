@@ -517,7 +517,7 @@ int sad_backward_noalloc(int H, int W, int N_cap, const float *records, const ui
  * dweights: float32 [T][K]; weights at empty slots are not read, dweights
  * there are 0.  Row matrices hold D elements of the given type (SAD_F32,
  * SAD_BF16, SAD_F16) per row, consecutive, with ld elements from one row to
- * the next (ld >= D); other arrays are dense.  Sums, dot products and
+ * the next (D <= ld < 2^30); other arrays are dense.  Sums, dot products and
  * statistics are float32; a result of a 16-bit type is rounded once, to
  * nearest even.  No float atomics: results are the same bits on every run
  * with the same sizes, types and alignment.

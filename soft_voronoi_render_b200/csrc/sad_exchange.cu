@@ -27,6 +27,27 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int K_MAX = 8;
 
+// row r of a matrix with `bytes` from row to row, column c: one multiply-add
+template <typename T> __device__ __forceinline__ const T *at_row(const T *base, uint32_t r, uint32_t bytes, int c) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base + c) + (unsigned long long)r * bytes);
+}
+
+// acc += w p
+template <typename T, int VEC>
+__device__ __forceinline__ void add_scaled(const Pack<T, VEC> &p, float w, Two (&acc)[(VEC + 1) / 2]) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2)
+        acc[i / 2] = fma_two(two(p.get(i), VEC > 1 ? p.get(i + (VEC > 1)) : 0.0f), two(w, w), acc[i / 2]);
+}
+// acc += p g
+template <typename T, int VEC>
+__device__ __forceinline__ void add_product(const Pack<T, VEC> &p, const Pack<T, VEC> &g, Two &acc) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2)
+        acc = fma_two(two(p.get(i), VEC > 1 ? p.get(i + (VEC > 1)) : 0.0f),
+                      two(g.get(i), VEC > 1 ? g.get(i + (VEC > 1)) : 0.0f), acc);
+}
+
 // the K ids and weights of row t; ids beyond K are empty slots
 template <bool FULL>
 __device__ __forceinline__ void load_slots(const int32_t *__restrict__ at, const float *__restrict__ w, long long t,
@@ -130,51 +151,73 @@ __device__ __forceinline__ void finish_dots(float (&dot)[K_MAX], int L, int lane
         if (i < count && first + i < K) dots[t * K + first + i] = dot[i];
 }
 
+// Empty slots are rows of zeros with weight 0, so that nothing branches
+// between the rows but the loads themselves.
 template <typename T, int VEC, bool FULL, bool SUM, bool DOT, bool ROW_PER_BLOCK>
-__global__ void __launch_bounds__(THREADS) gather_kernel(const T *__restrict__ R, long long ldr,
-                                                         const int32_t *__restrict__ at, uint32_t n_at,
-                                                         const float *__restrict__ w, const T *__restrict__ G,
-                                                         long long ldg, long long n_rows, int K, int D, int log_l,
-                                                         T *__restrict__ out, long long ldo,
-                                                         float *__restrict__ dots) {
+__global__ void __launch_bounds__(THREADS, SUM && DOT ? 3 : 4) gather_kernel(const T *__restrict__ R, uint32_t ldr,
+                                                            const int32_t *__restrict__ at, uint32_t n_at,
+                                                            const float *__restrict__ w, const T *__restrict__ G,
+                                                            uint32_t ldg, long long n_rows, int K, int D, int log_l,
+                                                            T *__restrict__ out, uint32_t ldo,
+                                                            float *__restrict__ dots) {
     const Lanes<VEC, ROW_PER_BLOCK> me(log_l, n_rows);
     uint32_t id[K_MAX];
-    float wt[K_MAX], dot[K_MAX] = {};
+    float wt[K_MAX], dot[K_MAX];
+    Two dots2[K_MAX];
     load_slots<FULL>(at, SUM ? w : nullptr, me.t, K, me.in, id, wt);
+#pragma unroll
+    for (int k = 0; k < K_MAX; ++k) {
+        if (id[k] >= n_at) wt[k] = 0.0f;
+        dots2[k] = two(0.0f, 0.0f);
+    }
     if (me.in) {
         for (int c = me.c0; c < D; c += me.step) {
             Pack<T, VEC> p[K_MAX];
 #pragma unroll
-            for (int k = 0; k < K_MAX; ++k)
-                if (id[k] < n_at) p[k] = load_pack<T, VEC>(R + (long long)id[k] * ldr + c);
-            float acc[VEC] = {};
+            for (int k = 0; k < K_MAX; ++k) {
+                p[k].clear();
+                if (id[k] < n_at) p[k] = load_pack<T, VEC>(at_row(R, id[k], ldr, c));
+            }
+            Two acc[(VEC + 1) / 2];
+#pragma unroll
+            for (int i = 0; i < (VEC + 1) / 2; ++i) acc[i] = two(0.0f, 0.0f);
             Pack<T, VEC> g;
-            if (DOT) g = load_pack<T, VEC>(G + me.t * ldg + c);
+            if (DOT) g = load_pack<T, VEC>(at_row(G, (uint32_t)me.t, ldg, c));
 #pragma unroll
             for (int k = 0; k < K_MAX; ++k) {
-                if (id[k] >= n_at) continue;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    if (SUM) acc[i] = fmaf(wt[k], p[k].get(i), acc[i]);
-                    if (DOT) dot[k] = fmaf(p[k].get(i), g.get(i), dot[k]);
-                }
+                if (SUM) add_scaled(p[k], wt[k], acc);
+                if (DOT) add_product(p[k], g, dots2[k]);
             }
             if (SUM) {
+                float f[VEC + 1];
+#pragma unroll
+                for (int i = 0; i < VEC; i += 2) both(acc[i / 2], f[i], f[i + 1]);
+                float v[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[i] = f[i];
                 Pack<T, VEC> o;
-                o.set(acc);
-                store_pack<T, VEC>(out + me.t * ldo + c, o);
+                o.set(v);
+                store_pack<T, VEC>(const_cast<T *>(at_row(out, (uint32_t)me.t, ldo, c)), o);
             }
         }
     }
-    if (DOT) finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
+    if (DOT) {
+#pragma unroll
+        for (int k = 0; k < K_MAX; ++k) {
+            float other;
+            both(dots2[k], dot[k], other);
+            dot[k] = id[k] < n_at ? dot[k] + other : 0.0f;  // G may hold infinities
+        }
+        finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
+    }
 }
 
 template <typename T, int VEC, bool FULL, bool DOT, bool ROW_PER_BLOCK>
-__global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X, long long ldx,
+__global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X, uint32_t ldx,
                                                          const int32_t *__restrict__ at, uint32_t n_at,
                                                          const float *__restrict__ w, const T *__restrict__ R,
-                                                         long long ldr, long long n_rows, int K, int D, int log_l,
-                                                         T *__restrict__ S, long long lds,
+                                                         uint32_t ldr, long long n_rows, int K, int D, int log_l,
+                                                         T *__restrict__ S, uint32_t lds,
                                                          float *__restrict__ dots) {
     const Lanes<VEC, ROW_PER_BLOCK> me(log_l, n_rows);
     uint32_t id[K_MAX];
@@ -185,13 +228,14 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
             Pack<T, VEC> p[K_MAX];
             if (DOT) {
 #pragma unroll
-                for (int k = 0; k < K_MAX; ++k)
-                    if (id[k] < n_at) p[k] = load_pack<T, VEC>(R + (long long)id[k] * ldr + c);
+                for (int k = 0; k < K_MAX; ++k) {
+                    p[k].clear();
+                    if (id[k] < n_at) p[k] = load_pack<T, VEC>(at_row(R, id[k], ldr, c));
+                }
             }
-            const Pack<T, VEC> x = load_pack<T, VEC>(X + me.t * ldx + c);
+            const Pack<T, VEC> x = load_pack<T, VEC>(at_row(X, (uint32_t)me.t, ldx, c));
 #pragma unroll
             for (int k = 0; k < K_MAX; ++k) {
-                if (id[k] >= n_at) continue;
                 float f[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
@@ -200,11 +244,15 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
                 }
                 Pack<T, VEC> o;
                 o.set(f);
-                store_pack<T, VEC>(S + (long long)id[k] * lds + c, o);
+                if (id[k] < n_at) store_pack<T, VEC>(const_cast<T *>(at_row(S, id[k], lds, c)), o);
             }
         }
     }
-    if (DOT) finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
+    if (DOT) {
+#pragma unroll
+        for (int k = 0; k < K_MAX; ++k) dot[k] = id[k] < n_at ? dot[k] : 0.0f;
+        finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -216,6 +264,13 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
 // joins the groups at the run's end.  A run that is all of its expert's pairs
 // goes to dF; one that is cut at the chunk's start or end goes to one of the
 // chunk's two partial rows, which join_kernel adds up in order.
+//
+// Every row of dout is read once for each of its K pairs.  Where dout does
+// not fit the L2 and ids are in no order over the rows (sites over an image),
+// chunks side by side in the list would read it from memory eight times
+// (3.2 GB for 2048 x 2048 x 32 bf16, 784 us): the chunks are then taken in
+// the order of their first pair's row, counted into BUCKETS parts of the
+// rows.  The order within a part is not fixed, and no result depends on it.
 // ---------------------------------------------------------------------------
 
 // the last e in [0, E) with offsets[e] <= s, for s below offsets[E]
@@ -230,18 +285,22 @@ __device__ __forceinline__ int expert_at(const int32_t *__restrict__ offsets, in
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ G, long long ldg,
+__global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ G, uint32_t ldg,
                                                           const float *__restrict__ w,
                                                           const int32_t *__restrict__ offsets,
                                                           const int32_t *__restrict__ order, uint32_t n, int K, int E,
                                                           int D, int log_l, uint32_t C, uint32_t chunks,
-                                                          float *__restrict__ dF, float *__restrict__ partial) {
+                                                          const uint32_t *__restrict__ turn,
+                                                          float *__restrict__ dF, float *__restrict__ partial,
+                                                          int32_t *__restrict__ cut_expert) {
     const int L = 1 << log_l, S = 32 >> log_l;
     const int lane = threadIdx.x & 31, sub = lane >> log_l, in_row = lane & (L - 1);
-    const uint32_t chunk = (uint32_t)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
+    uint32_t chunk = (uint32_t)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
     if (chunk >= chunks) return;
+    if (turn) chunk = min(__ldg(turn + chunk), chunks - 1);
     const uint32_t total = min((uint32_t)__ldg(offsets + E), n);
     const uint32_t lo = chunk * C;
+    if (lane == 0 && blockIdx.y == 0) cut_expert[chunk] = -1;
     if (lo >= total) return;
     const uint32_t hi = min(lo + C, total);
     const int first = expert_at(offsets, E, lo);
@@ -257,7 +316,9 @@ __global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ 
                 continue;
             }
             const uint32_t b = min(end, hi);
-            float acc[VEC] = {};
+            Two acc2[(VEC + 1) / 2];
+#pragma unroll
+            for (int i = 0; i < (VEC + 1) / 2; ++i) acc2[i] = two(0.0f, 0.0f);
             for (uint32_t s = a; s < b; s += 32) {
                 uint32_t row = 0;
                 float wj = 0.0f;
@@ -277,23 +338,25 @@ __global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ 
                         const uint32_t at = q + u * S + sub;
                         const uint32_t r = __shfl_sync(0xffffffffu, row, at & 31);
                         wq[u] = __shfl_sync(0xffffffffu, wj, at & 31);
-                        if (at < left && col) p[u] = load_pack<T, VEC>(G + (long long)r * ldg + c);
+                        p[u].clear();
+                    if (at < left && col) p[u] = load_pack<T, VEC>(at_row(G, r, ldg, c));
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        if (q + u * S + sub < left && col) {
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i) acc[i] = fmaf(wq[u], p[u].get(i), acc[i]);
-                        }
-                    }
+                    for (int u = 0; u < 4; ++u) add_scaled(p[u], wq[u], acc2);  // 0 beyond the run
                 }
             }
+            float acc[VEC + 1];
+#pragma unroll
+            for (int i = 0; i < VEC; i += 2) both(acc2[i / 2], acc[i], acc[i + 1]);
             for (int o = L; o < 32; o <<= 1) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
             }
             if (sub == 0 && col) {
-                const bool whole = (uint32_t)__ldg(offsets + e) == a && end == b;
+                const uint32_t from = (uint32_t)__ldg(offsets + e);
+                const bool whole = from == a && end == b;
+                // the expert that starts in this chunk and goes on behind it
+                if (lane == 0 && slab == 0 && from >= lo && end > b) cut_expert[chunk] = e;
                 float *to = whole ? dF + (long long)e * D + c
                                   : partial + ((size_t)2 * chunk + (a == lo ? 0 : 1)) * D + c;
                 Pack<float, VEC % 4 ? VEC : 4> f;
@@ -314,46 +377,104 @@ __global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ 
     }
 }
 
-// a block per chunk: where an expert's pairs start in the chunk (or at its
-// first position) and reach beyond it, adds up that expert's partial rows
-__global__ void __launch_bounds__(THREADS) join_kernel(const int32_t *__restrict__ offsets, uint32_t n, int E, int D,
-                                                       uint32_t C, const float *__restrict__ partial,
-                                                       float *__restrict__ dF) {
-    __shared__ int expert;
+// For each chunk's expert that starts in it and goes on behind it: the sum of
+// that expert's partial rows, from this chunk's to the one that it ends in.
+// A warp a chunk; experts of more than LONG chunks are left to the block,
+// whose warps take a run of the rows each.
+constexpr uint32_t LONG = 32;
+__global__ void __launch_bounds__(THREADS) join_kernel(const int32_t *__restrict__ offsets,
+                                                       const int32_t *__restrict__ cut_expert, uint32_t n, int E,
+                                                       int D, uint32_t C, uint32_t chunks,
+                                                       const float *__restrict__ partial, float *__restrict__ dF) {
+    __shared__ uint32_t long_chunk[WARPS];
     __shared__ float part[WARPS][33];
-    const uint32_t chunk = blockIdx.x, lo = chunk * C;
-    const uint32_t total = min((uint32_t)__ldg(offsets + E), n);
-    if (total <= lo || total - lo <= C) return;  // nothing reaches beyond the last chunk
-    if (threadIdx.x == 0) expert = expert_at(offsets, E, lo + C - 1);
-    __syncthreads();
-    const int e = expert;
-    const uint32_t from = (uint32_t)__ldg(offsets + e), end = min((uint32_t)__ldg(offsets + e + 1), total);
-    if (from < lo || end <= lo + C) return;  // started earlier, or ends here
-    const uint32_t last = (end - 1) / C;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int c0 = 0; c0 < D; c0 += 32) {
-        const int c = c0 + lane;
-        float s = 0.0f;
-        if (c < D) {
-            // rows chunk .. last in runs of a warp each
-            const uint32_t count = last - chunk + 1, each = (count + WARPS - 1) / WARPS;
-            const uint32_t q0 = chunk + warp * each, q1 = min(q0 + each, last + 1);
-#pragma unroll 8
-            for (uint32_t q = q0; q < q1; ++q) {
-                const int slot = q == chunk && from != lo ? 1 : 0;
-                s += __ldg(partial + ((size_t)2 * q + slot) * D + c);
-            }
+    auto span = [&](uint32_t chunk, int &e, uint32_t &last, int &slot) {
+        e = __ldg(cut_expert + chunk);
+        if (e < 0) return;
+        const uint32_t end = min((uint32_t)__ldg(offsets + e + 1), n);
+        last = min((end - 1) / C, chunks - 1);
+        slot = (uint32_t)__ldg(offsets + e) != chunk * C;  // where its first run was put
+    };
+    auto row = [&](uint32_t q, uint32_t chunk, int slot) {
+        return partial + ((size_t)2 * q + (q == chunk ? slot : 0)) * D;
+    };
+    const uint32_t chunk = blockIdx.x * WARPS + warp;
+    int e = -1, slot = 0;
+    uint32_t last = 0;
+    if (chunk < chunks) span(chunk, e, last, slot);
+    const bool later = e >= 0 && last - chunk >= LONG;
+    if (lane == 0) long_chunk[warp] = later ? chunk : 0xffffffffu;
+    if (e >= 0 && !later) {
+        for (int c = lane; c < D; c += 32) {
+            float s = 0.0f;
+#pragma unroll 4
+            for (uint32_t q = chunk; q <= last; ++q) s += __ldg(row(q, chunk, slot) + c);
+            dF[(long long)e * D + c] = s;
         }
-        part[warp][lane] = s;
-        __syncthreads();
-        if (warp == 0 && c < D) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int q = 0; q < WARPS; ++q) sum += part[q][lane];
-            dF[(long long)e * D + c] = sum;
-        }
-        __syncthreads();
     }
+    __syncthreads();
+    for (int k = 0; k < WARPS; ++k) {
+        const uint32_t from = long_chunk[k];
+        if (from == 0xffffffffu) continue;
+        span(from, e, last, slot);
+        const uint32_t each = (last - from + WARPS) / WARPS, q0 = from + warp * each, q1 = min(q0 + each, last + 1);
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            const int c = c0 + lane;
+            float s = 0.0f;
+            if (c < D) {
+#pragma unroll 8
+                for (uint32_t q = q0; q < q1; ++q) s += __ldg(row(q, from, slot) + c);
+            }
+            part[warp][lane] = s;
+            __syncthreads();
+            if (warp == 0 && c < D) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < WARPS; ++q) sum += part[q][lane];
+                dF[(long long)e * D + c] = sum;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// the order in which chunks are taken: a count of each part of the rows, its
+// scan, and the chunks put into their part's places
+constexpr int BUCKETS = 4096;
+__device__ __forceinline__ uint32_t bucket_of(const int32_t *__restrict__ order, uint32_t chunk, uint32_t C, uint32_t n) {
+    const uint32_t j = (uint32_t)__ldg(order + (size_t)chunk * C);
+    return j < n ? (uint32_t)((unsigned long long)j * BUCKETS / n) : BUCKETS - 1;  // behind the last pair: last
+}
+__global__ void __launch_bounds__(THREADS) turn_count_kernel(const int32_t *__restrict__ order, uint32_t n, uint32_t C,
+                                                             uint32_t chunks, uint32_t *__restrict__ count) {
+    const uint32_t chunk = blockIdx.x * THREADS + threadIdx.x;
+    if (chunk < chunks) atomicAdd(count + bucket_of(order, chunk, C, n), 1u);
+}
+__global__ void __launch_bounds__(1024) turn_scan_kernel(uint32_t *__restrict__ count) {
+    __shared__ uint32_t warp_total[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint4 v = reinterpret_cast<uint4 *>(count)[threadIdx.x];
+    const uint32_t mine = v.x + v.y + v.z + v.w;
+    uint32_t s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+    }
+    if (lane == 31) warp_total[warp] = s;
+    __syncthreads();
+    uint32_t before = s - mine;
+    for (int q = 0; q < warp; ++q) before += warp_total[q];
+    const uint4 o = make_uint4(before, before + v.x, before + v.x + v.y, before + v.x + v.y + v.z);
+    reinterpret_cast<uint4 *>(count)[threadIdx.x] = o;
+}
+static_assert(BUCKETS == 4 * 1024, "turn_scan_kernel takes four counts a thread");
+__global__ void __launch_bounds__(THREADS) turn_place_kernel(const int32_t *__restrict__ order, uint32_t n, uint32_t C,
+                                                             uint32_t chunks, uint32_t *__restrict__ next,
+                                                             uint32_t *__restrict__ turn) {
+    const uint32_t chunk = blockIdx.x * THREADS + threadIdx.x;
+    if (chunk < chunks) turn[atomicAdd(next + bucket_of(order, chunk, C, n), 1u)] = chunk;
 }
 
 int ceil_log2(int v) {
@@ -367,6 +488,9 @@ int group_log(int D, int vec) {
     const int pieces = (D + vec - 1) / vec;
     return pieces >= 32 ? 5 : ceil_log2(pieces);
 }
+
+// a row distance below 2^30 elements, in bytes
+template <typename T> uint32_t row_bytes(long long ld) { return (uint32_t)(ld * (long long)sizeof(T)); }
 
 struct Shape {
     unsigned blocks;
@@ -386,9 +510,10 @@ Shape shape_of(long long n, int D, int vec) {
 }
 
 template <typename T, int VEC, bool FULL, bool SUM, bool DOT>
-void gather_launch(const Shape &s, const T *R, long long ldr, const int32_t *at, uint32_t n_at, const float *w,
-                   const T *G, long long ldg, long long n, int K, int D, T *out, long long ldo, float *dots,
+void gather_launch(const Shape &s, const T *R, long long ld_rows, const int32_t *at, uint32_t n_at, const float *w,
+                   const T *G, long long ld_other, long long n, int K, int D, T *out, long long ld_out, float *dots,
                    cudaStream_t st) {
+    const uint32_t ldr = row_bytes<T>(ld_rows), ldg = row_bytes<T>(ld_other), ldo = row_bytes<T>(ld_out);
     if (s.row_per_block)
         gather_kernel<T, VEC, FULL, SUM, DOT, true><<<s.blocks, THREADS, 0, st>>>(R, ldr, at, n_at, w, G, ldg, n, K, D,
                                                                                   5, out, ldo, dots);
@@ -421,9 +546,10 @@ cudaError_t gather(RowsIn rows, const int32_t *at, long long n_at, const float *
 }
 
 template <typename T, int VEC, bool FULL, bool DOT>
-void spread_launch(const Shape &s, const T *X, long long ldx, const int32_t *at, uint32_t n_at, const float *w,
-                   const T *R, long long ldr, long long n, int K, int D, T *S, long long lds, float *dots,
+void spread_launch(const Shape &s, const T *X, long long ld_x, const int32_t *at, uint32_t n_at, const float *w,
+                   const T *R, long long ld_rows, long long n, int K, int D, T *S, long long ld_to, float *dots,
                    cudaStream_t st) {
+    const uint32_t ldx = row_bytes<T>(ld_x), ldr = row_bytes<T>(ld_rows), lds = row_bytes<T>(ld_to);
     if (s.row_per_block)
         spread_kernel<T, VEC, FULL, DOT, true><<<s.blocks, THREADS, 0, st>>>(X, ldx, at, n_at, w, R, ldr, n, K, D, 5,
                                                                              S, lds, dots);
@@ -482,22 +608,58 @@ uint32_t chunk_of(long long n, int E) {
     return (uint32_t)c;
 }
 
+// dout beyond half of the L2
+constexpr size_t FAR_BYTES = 64u << 20;
+
+size_t up(size_t v) { return (v + 255) & ~size_t(255); }
+
+// workspace: partial rows, experts cut, then counts and turns of the chunks
+struct Space {
+    float *partial;
+    int32_t *cut_expert;
+    uint32_t *count, *turn;
+    size_t bytes;
+    Space(void *ws, uint32_t chunks, int D) {
+        char *p = static_cast<char *>(ws);
+        partial = reinterpret_cast<float *>(p);
+        size_t at = up(sizeof(float) * 2 * (size_t)chunks * D);
+        cut_expert = reinterpret_cast<int32_t *>(p + at);
+        at += up(sizeof(int32_t) * (size_t)chunks);
+        count = reinterpret_cast<uint32_t *>(p + at);
+        at += sizeof(uint32_t) * BUCKETS;
+        turn = reinterpret_cast<uint32_t *>(p + at);
+        bytes = at + up(sizeof(uint32_t) * (size_t)chunks);
+    }
+};
+
 template <typename T, int VEC>
 cudaError_t segments(RowsIn g, const float *w, const int32_t *offsets, const int32_t *order, long long n, int K,
-                     int E, int D, float *dF, float *partial, cudaStream_t st) {
+                     int E, int D, float *dF, void *ws, cudaStream_t st) {
     const uint32_t C = chunk_of(n, E), chunks = (uint32_t)((n + C - 1) / C);
+    const Space s(ws, chunks, D);
+    const bool far = (size_t)(n / K) * D * sizeof(T) > FAR_BYTES;
+    if (far) {
+        const cudaError_t e = cudaMemsetAsync(s.count, 0, sizeof(uint32_t) * BUCKETS, st);
+        if (e != cudaSuccess) return e;
+        const unsigned blocks = (chunks + THREADS - 1) / THREADS;
+        turn_count_kernel<<<blocks, THREADS, 0, st>>>(order, (uint32_t)n, C, chunks, s.count);
+        turn_scan_kernel<<<1, 1024, 0, st>>>(s.count);
+        turn_place_kernel<<<blocks, THREADS, 0, st>>>(order, (uint32_t)n, C, chunks, s.count, s.turn);
+    }
     const dim3 grid((chunks + WARPS - 1) / WARPS, (unsigned)min((D + 32 * VEC - 1) / (32 * VEC), 65535));
-    segment_kernel<T, VEC><<<grid, THREADS, 0, st>>>(static_cast<const T *>(g.p), g.ld, w, offsets, order,
-                                                     (uint32_t)n, K, E, D, group_log(D, VEC), C, chunks, dF, partial);
-    if (chunks > 1) join_kernel<<<chunks - 1, THREADS, 0, st>>>(offsets, (uint32_t)n, E, D, C, partial, dF);
+    segment_kernel<T, VEC><<<grid, THREADS, 0, st>>>(static_cast<const T *>(g.p), row_bytes<T>(g.ld), w, offsets,
+                                                     order, (uint32_t)n, K, E, D, group_log(D, VEC), C, chunks,
+                                                     far ? s.turn : nullptr, dF, s.partial, s.cut_expert);
+    if (chunks > 1)
+        join_kernel<<<(chunks + WARPS - 1) / WARPS, THREADS, 0, st>>>(offsets, s.cut_expert, (uint32_t)n, E, D, C,
+                                                                      chunks, s.partial, dF);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t segments_typed(RowsIn g, const float *w, const int32_t *offsets, const int32_t *order, long long n,
-                           int K, int E, int D, float *dF, float *partial, cudaStream_t st) {
-    return BY_PIECE(T, piece_bytes(g.p, g.ld, D, sizeof(T)), segments, g, w, offsets, order, n, K, E, D, dF, partial,
-                    st);
+                           int K, int E, int D, float *dF, void *ws, cudaStream_t st) {
+    return BY_PIECE(T, piece_bytes(g.p, g.ld, D, sizeof(T)), segments, g, w, offsets, order, n, K, E, D, dF, ws, st);
 }
 
 }  // namespace
@@ -519,7 +681,7 @@ cudaError_t launch_spread(int dtype, RowsIn x, const int32_t *at, long long n_at
 size_t segment_workspace_bytes(long long n_rows, int K, int E, int D) {
     const long long n = n_rows * K;
     const uint32_t C = chunk_of(n, E);
-    return sizeof(float) * 2 * (size_t)((n + C - 1) / C) * D;
+    return Space(nullptr, (uint32_t)((n + C - 1) / C), D).bytes;
 }
 
 cudaError_t launch_segment_sums(int dtype, RowsIn dout, const float *w, const int32_t *offsets, const int32_t *order,
@@ -527,11 +689,10 @@ cudaError_t launch_segment_sums(int dtype, RowsIn dout, const float *w, const in
     // experts without pairs
     const cudaError_t e = cudaMemsetAsync(dF, 0, sizeof(float) * (size_t)E * D, st);
     if (e != cudaSuccess) return e;
-    float *p = static_cast<float *>(ws);
     const long long n = T * K;
-    if (dtype == 0) return segments_typed<float>(dout, w, offsets, order, n, K, E, D, dF, p, st);
-    if (dtype == 1) return segments_typed<__nv_bfloat16>(dout, w, offsets, order, n, K, E, D, dF, p, st);
-    return segments_typed<__half>(dout, w, offsets, order, n, K, E, D, dF, p, st);
+    if (dtype == 0) return segments_typed<float>(dout, w, offsets, order, n, K, E, D, dF, ws, st);
+    if (dtype == 1) return segments_typed<__nv_bfloat16>(dout, w, offsets, order, n, K, E, D, dF, ws, st);
+    return segments_typed<__half>(dout, w, offsets, order, n, K, E, D, dF, ws, st);
 }
 
 }  // namespace sad

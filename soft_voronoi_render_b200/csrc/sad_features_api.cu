@@ -49,7 +49,8 @@ int check_rows(const char *name, int dtype, const void *p, int64_t ld, int D) {
     if (!p) return bad(SAD_ERR_INVALID_ARG, "%s is NULL", name);
     if (!aligned(p, element_bytes(dtype))) return bad(SAD_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
     if (ld < D) return bad(SAD_ERR_INVALID_ARG, "%s: %lld elements between rows of %d", name, (long long)ld, D);
-    if (ld > (1ll << 40)) return bad(SAD_ERR_INVALID_ARG, "%s: row distance %lld is too large", name, (long long)ld);
+    // the kernels count a row's bytes in 32 bits
+    if (ld >= (1ll << 30)) return bad(SAD_ERR_INVALID_ARG, "%s: row distance %lld is too large", name, (long long)ld);
     return SAD_OK;
 }
 

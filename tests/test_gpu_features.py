@@ -627,3 +627,52 @@ def test_feature_field_fit():
     assert len(losses) == 3 and all(np.isfinite(losses))
     assert fit.run_features(field, tid, tl, iterations=0) == []
     s.close()
+
+
+@pytest.mark.parametrize("D", [4, 64, 65, 300])
+def test_empty_slots_beside_infinities(D):
+    """Gradients of empty slots are 0 and rows without pairs give 0, also
+    where the row that comes back holds infinities or NaN."""
+    f = feat()
+    g = rng(D)
+    T, K, E = 40, 8, 9
+    ids = make_ids(g, T, K, E, 0.4)
+    w = torch.rand((T, K), generator=g, device="cuda")
+    F, dout = randn(g, E, D), randn(g, T, D)
+    dout[::3] = float("inf")
+    dout[1::3] = float("nan")
+    r = f.Route(T, K, E).build(ids)
+    empty = r.place < 0
+    _, dw = f.blend_backward(dout, F, ids, w, r)
+    assert bool((dw[empty] == 0).all()) and not bool(torch.isfinite(dw[::3][~empty[::3]]).any())
+    y = randn(g, T * K, D)
+    for dw in (r.combine_backward(dout, y, w)[1], r.dispatch_backward(y, dout, w)[1]):
+        assert bool((dw[empty] == 0).all())
+        assert bool(torch.isfinite(dw[2::3]).all())
+
+
+@pytest.mark.parametrize("T,E,D,dt", [(300000, 3000, 64, "f32"), (400001, 5, 48, "f32"), (262144, 200000, 70, "bf16"),
+                                      (1100000, 40000, 33, "f16")])
+def test_blend_backward_beyond_the_cache(T, E, D, dt):
+    """Enough rows that the chunks are taken in the order of the rows: the
+    same sums, sites with few, many and no pairs among them."""
+    f, t = feat(), TYPES[dt]
+    g = rng(T)
+    ids = make_ids(g, T, 8, E, 0.05)
+    valid = (ids >= 0) & (ids < E)
+    w = torch.rand((T, 8), generator=g, device="cuda")
+    dout = randn(g, T, D, dtype=t)
+    F = randn(g, E, D, dtype=t)
+    r = f.Route(T, 8, E).build(ids)
+    dF, dw = f.blend_backward(dout, F, ids, w, r)
+    ref, big = torch.zeros((E, D), device="cuda").double(), torch.zeros((E, D), device="cuda").double()
+    for k in range(8):
+        s = dout.double() * torch.where(valid[:, k], w[:, k].double(), 0.0)[:, None]
+        at = torch.where(valid[:, k], ids[:, k], 0).long()
+        ref.index_add_(0, at, s)
+        big.index_add_(0, at, s.abs())
+    count = (r.offsets[1:] - r.offsets[:-1])[:, None].double()
+    # chunks of at most 4096 pairs, then at most 8192 partial rows by eight warps
+    close(dF, ref, torch.minimum(count + 1, torch.tensor(4096.0 + 1100, device="cuda").double()) * U * big)
+    dF2, dw2 = f.blend_backward(dout, F, ids, w, r)
+    assert torch.equal(dF, dF2) and torch.equal(dw, dw2)
