@@ -8,6 +8,15 @@
 // MAX_BITS bits as that takes.  A pass counts each block's digits, scans the
 // counts digit by digit, and ranks every item inside its warp by match
 // masks, which keeps pairs of one expert in their order without atomics.
+//
+// Several passes over many pairs are bound by their scattered writes: in the
+// last one the pairs come in the order of their low digit, and each writes 4
+// bytes of place to a sector of its own (2048 x 2048 x 8 pairs, 131,072 sites:
+// 490 us for 1.6 GB).  Candidate lists are coherent, though: 4096 pairs of
+// neighbouring rows hold a few hundred sites.  So there the pairs are sorted
+// within tiles of 4096 first, in shared memory; only the tiles' runs of one
+// expert (about 15 pairs each) are sorted by the passes above; and every tile
+// then writes its part of order and place, in the pairs' own order.
 #include "sad_features.h"
 
 namespace sad {
@@ -25,7 +34,14 @@ struct Plan {
     int passes, bits;     // digits of `bits` bits
     int blocks;
     long long per_block;  // items, a multiple of TILE
+    bool by_runs;
 };
+
+// tiles that are sorted in shared memory, and the pairs from which on they
+// are: below, their dozen launches cost more than the scattered writes
+constexpr int RUN_ITEMS = 16;
+constexpr int RUN_TILE = THREADS * RUN_ITEMS;
+constexpr long long RUN_PAIRS = 1 << 20;
 
 Plan make_plan(long long n, int E) {
     int key_bits = 1;
@@ -33,6 +49,7 @@ Plan make_plan(long long n, int E) {
     Plan p;
     p.passes = (key_bits + MAX_BITS - 1) / MAX_BITS;
     p.bits = (key_bits + p.passes - 1) / p.passes;
+    p.by_runs = p.passes > 1 && n >= RUN_PAIRS;
     const long long tiles = (n + TILE - 1) / TILE;
     p.blocks = (int)(tiles < MAX_BLOCKS ? (tiles ? tiles : 1) : MAX_BLOCKS);
     const long long tpb = (tiles + p.blocks - 1) / p.blocks;
@@ -48,12 +65,22 @@ __device__ __forceinline__ uint32_t key_of(int32_t id, int E) {
     return (uint32_t)id < (uint32_t)E ? (uint32_t)id : (uint32_t)E;
 }
 
+// items and items a block of a list whose length only the device knows
+__device__ __forceinline__ void list_length(const uint32_t *__restrict__ length, long long &n, long long &per_block) {
+    if (!length) return;
+    n = min((long long)__ldg(length), n);
+    const long long tiles = (n + TILE - 1) / TILE;
+    per_block = (tiles + gridDim.x - 1) / gridDim.x * TILE;
+}
+
 // counts[digit][block]
 __global__ void __launch_bounds__(THREADS) count_kernel(const int32_t *__restrict__ ids,
                                                         const uint32_t *__restrict__ keys, long long n, int E,
                                                         long long per_block, int shift, int bits,
-                                                        uint32_t *__restrict__ counts) {
+                                                        uint32_t *__restrict__ counts,
+                                                        const uint32_t *__restrict__ length) {
     extern __shared__ uint32_t hist[];
+    list_length(length, n, per_block);
     const int D = 1 << bits;
     for (int d = threadIdx.x; d < D; d += THREADS) hist[d] = 0;
     __syncthreads();
@@ -132,8 +159,10 @@ __global__ void __launch_bounds__(THREADS) move_kernel(const int32_t *__restrict
                                                        uint32_t *__restrict__ keys_out,
                                                        uint32_t *__restrict__ pairs_out,
                                                        int32_t *__restrict__ order, int32_t *__restrict__ place,
-                                                       int32_t *__restrict__ offsets) {
+                                                       int32_t *__restrict__ offsets,
+                                                       const uint32_t *__restrict__ length) {
     extern __shared__ uint32_t smem[];
+    list_length(length, n, per_block);
     __shared__ uint32_t warp_sum[WARPS];
     const int D = 1 << bits;
     uint32_t *base = smem;            // [D] next global position of each digit
@@ -213,11 +242,399 @@ __global__ void __launch_bounds__(THREADS) offsets_kernel(const int32_t *__restr
     offsets[e] = (int32_t)lo;
 }
 
+// ---------------------------------------------------------------------------
+// by runs
+// ---------------------------------------------------------------------------
+// Sorts a tile of pairs by key in shared memory, stable.  Writes the pairs'
+// places in the tile in sorted order (local), a bit for every place where
+// another key starts (heads), and for every run its key and first place; runs
+// of tile t are entries t RUN_TILE + 0, 1, ...
+__global__ void __launch_bounds__(THREADS, 3) tile_sort_kernel(const int32_t *__restrict__ ids, long long n, int E,
+                                                            int passes, int bits, uint16_t *__restrict__ local,
+                                                            uint32_t *__restrict__ heads,
+                                                            uint32_t *__restrict__ run_key,
+                                                            uint16_t *__restrict__ run_start,
+                                                            uint32_t *__restrict__ run_count) {
+    extern __shared__ uint32_t smem[];
+    __shared__ uint32_t warp_sum[WARPS];
+    constexpr int WORDS = RUN_TILE / 32;
+    __shared__ uint32_t word[WORDS], before[WORDS];
+    const int D = 1 << bits;
+    uint32_t *keys = smem;                                            // [RUN_TILE]
+    uint16_t *at = reinterpret_cast<uint16_t *>(smem + RUN_TILE);     // [RUN_TILE]
+    uint16_t *wc = at + RUN_TILE;                                     // [WARPS][D]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t0 = (long long)blockIdx.x * RUN_TILE;
+    const int count = (int)min((long long)RUN_TILE, n - t0);
+    const int p0 = warp * (32 * RUN_ITEMS) + lane;  // this thread's places: p0 + 32 q
+    uint32_t key[RUN_ITEMS];
+    uint16_t idx[RUN_ITEMS];
+#pragma unroll
+    for (int q = 0; q < RUN_ITEMS; ++q) {
+        const int p = p0 + 32 * q;
+        key[q] = p < count ? key_of(__ldg(ids + t0 + p), E) : 0xffffffffu;
+        idx[q] = (uint16_t)p;
+    }
+    uint16_t *mine = wc + warp * D;
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * bits;
+        for (int d = lane; d < D / 2; d += 32) reinterpret_cast<uint32_t *>(mine)[d] = 0;
+        __syncwarp();
+        uint16_t rank[RUN_ITEMS];
+#pragma unroll
+        for (int q = 0; q < RUN_ITEMS; ++q) {
+            // places beyond the last pair have the largest digits and come last, so stay last
+            const uint32_t d = key[q] >> shift & (D - 1);
+            const unsigned peers = __match_any_sync(0xffffffffu, d);
+            const unsigned below = peers & ((1u << lane) - 1);
+            const uint32_t old = mine[d];
+            __syncwarp();
+            if (below == 0) mine[d] = (uint16_t)(old + __popc(peers));
+            __syncwarp();
+            rank[q] = (uint16_t)(old + __popc(below));
+        }
+        __syncthreads();
+        // starts of the warps' items: digits in order, warps in order
+        uint32_t carry = 0;
+        for (int d0 = 0; d0 < D; d0 += THREADS) {
+            const int d = d0 + threadIdx.x;
+            uint32_t total = 0;
+            if (d < D) {
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) total += wc[w * D + d];
+            }
+            uint32_t s = total;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += u;
+            }
+            if (lane == 31) warp_sum[warp] = s;
+            __syncthreads();
+            uint32_t start = carry + s - total;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                if (w < warp) start += warp_sum[w];
+                carry += warp_sum[w];
+            }
+            if (d < D) {
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) {
+                    const uint32_t c = wc[w * D + d];
+                    wc[w * D + d] = (uint16_t)start;
+                    start += c;
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int q = 0; q < RUN_ITEMS; ++q) {
+            const int to = mine[key[q] >> shift & (D - 1)] + rank[q];
+            keys[to] = key[q];
+            at[to] = idx[q];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < RUN_ITEMS; ++q) {
+            key[q] = keys[p0 + 32 * q];
+            idx[q] = at[p0 + 32 * q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < RUN_ITEMS; ++q) {
+        const int p = p0 + 32 * q;
+        const bool head = p < count && (p == 0 || keys[p - 1] != key[q]);
+        const uint32_t b = __ballot_sync(0xffffffffu, head);
+        if (lane == 0) word[p >> 5] = b;
+        if (p < count) local[t0 + p] = idx[q];
+    }
+    __syncthreads();
+    static_assert(WORDS == 4 * 32, "one warp scans four words a lane");
+    if (warp == 0) {
+        uint32_t c[4], s = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) c[u] = __popc(word[lane * 4 + u]), s += c[u];
+        const uint32_t sum = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        uint32_t b = s - sum;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            before[lane * 4 + u] = b;
+            b += c[u];
+        }
+        if (lane == 31) run_count[blockIdx.x] = s;
+    }
+    if (threadIdx.x < WORDS) heads[(size_t)blockIdx.x * WORDS + threadIdx.x] = word[threadIdx.x];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < RUN_ITEMS; ++q) {
+        const int p = p0 + 32 * q;
+        const uint32_t b = word[p >> 5];
+        if (!(b >> lane & 1u)) continue;
+        const uint32_t r = before[p >> 5] + __popc(b & ((1u << lane) - 1));
+        run_key[t0 + r] = key[q];
+        run_start[t0 + r] = (uint16_t)p;
+    }
+}
+
+// base[t] = runs of the tiles before t; base[tiles] = all
+__global__ void __launch_bounds__(1024) run_base_kernel(const uint32_t *__restrict__ run_count, int tiles,
+                                                        uint32_t *__restrict__ base) {
+    __shared__ uint32_t warp_sum[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t carry = 0;
+    for (int t0 = 0; t0 < tiles; t0 += 1024) {
+        const int t = t0 + threadIdx.x;
+        const uint32_t v = t < tiles ? run_count[t] : 0;
+        uint32_t s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) warp_sum[warp] = s;
+        __syncthreads();
+        uint32_t start = carry + s - v;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) start += warp_sum[w];
+            carry += warp_sum[w];
+        }
+        if (t < tiles) base[t] = start;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) base[tiles] = carry;
+}
+
+// the runs of all tiles behind one another: key, and the run's entry
+__global__ void __launch_bounds__(THREADS) run_list_kernel(const uint32_t *__restrict__ run_key,
+                                                           const uint32_t *__restrict__ base,
+                                                           uint32_t *__restrict__ key, uint32_t *__restrict__ entry) {
+    const uint32_t from = base[blockIdx.x], count = base[blockIdx.x + 1] - from;
+    const uint32_t t0 = blockIdx.x * (uint32_t)RUN_TILE;
+    for (uint32_t r = threadIdx.x; r < count; r += THREADS) {
+        key[from + r] = run_key[t0 + r];
+        entry[from + r] = t0 + r;
+    }
+}
+
+// pairs in the run of an entry
+__device__ __forceinline__ uint32_t run_length(uint32_t entry, const uint16_t *__restrict__ run_start,
+                                               const uint32_t *__restrict__ run_count, long long n) {
+    const uint32_t t = entry / RUN_TILE, r = entry % RUN_TILE;
+    const uint32_t end = r + 1 < run_count[t] ? run_start[entry + 1]
+                                              : (uint32_t)min((long long)RUN_TILE, n - (long long)t * RUN_TILE);
+    return end - run_start[entry];
+}
+
+// The sorted runs' first positions: a run of runs a block, its sum first,
+// then its scan behind the sums of the blocks before it.  where[entry] is the
+// position for the tiles, sorted[i] the same by rank for the offsets.
+__global__ void __launch_bounds__(THREADS) run_sum_kernel(const uint32_t *__restrict__ entry,
+                                                          const uint32_t *__restrict__ length,
+                                                          const uint16_t *__restrict__ run_start,
+                                                          const uint32_t *__restrict__ run_count, long long n,
+                                                          uint32_t *__restrict__ sums) {
+    __shared__ uint32_t warp_sum[WARPS];
+    const uint32_t total = *length, each = (total + gridDim.x - 1) / gridDim.x;
+    const uint32_t lo = min(blockIdx.x * each, total), hi = min(lo + each, total);
+    uint32_t s = 0;
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += THREADS) s += run_length(entry[i], run_start, run_count, n);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0;
+        for (int w = 0; w < WARPS; ++w) s += warp_sum[w];
+        sums[blockIdx.x] = s;
+    }
+}
+__global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__restrict__ entry,
+                                                            const uint32_t *__restrict__ length,
+                                                            const uint16_t *__restrict__ run_start,
+                                                            const uint32_t *__restrict__ run_count, long long n,
+                                                            const uint32_t *__restrict__ sums,
+                                                            uint32_t *__restrict__ where,
+                                                            uint32_t *__restrict__ sorted) {
+    __shared__ uint32_t warp_sum[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t total = *length, each = (total + gridDim.x - 1) / gridDim.x;
+    const uint32_t lo = min(blockIdx.x * each, total), hi = min(lo + each, total);
+    uint32_t carry = 0;
+    for (int b = threadIdx.x; b < blockIdx.x; b += THREADS) carry += sums[b];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) carry += __shfl_xor_sync(0xffffffffu, carry, o);
+    if (lane == 0) warp_sum[warp] = carry;
+    __syncthreads();
+    carry = 0;
+    for (int w = 0; w < WARPS; ++w) carry += warp_sum[w];
+    __syncthreads();
+    for (uint32_t i0 = lo; i0 < hi; i0 += THREADS) {
+        const uint32_t i = i0 + threadIdx.x;
+        const uint32_t e = i < hi ? entry[i] : 0, v = i < hi ? run_length(e, run_start, run_count, n) : 0;
+        uint32_t s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) warp_sum[warp] = s;
+        __syncthreads();
+        uint32_t start = carry + s - v;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) start += warp_sum[w];
+            carry += warp_sum[w];
+        }
+        if (i < hi) {
+            where[e] = start;
+            sorted[i] = start;
+        }
+        __syncthreads();
+    }
+}
+
+// offsets[e]: the first position of the first run with a key of e or more
+__global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__restrict__ key,
+                                                              const uint32_t *__restrict__ sorted,
+                                                              const uint32_t *__restrict__ length, long long n, int E,
+                                                              int32_t *__restrict__ offsets) {
+    const int e = blockIdx.x * THREADS + threadIdx.x;
+    if (e > E) return;
+    const uint32_t total = *length;
+    uint32_t lo = 0, hi = total;
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (__ldg(key + mid) < (uint32_t)e) lo = mid + 1;
+        else hi = mid;
+    }
+    offsets[e] = (int32_t)(lo < total ? sorted[lo] : (uint32_t)n);
+}
+
+// a tile's part of order and place
+__global__ void __launch_bounds__(THREADS) tile_write_kernel(long long n, const uint16_t *__restrict__ local,
+                                                             const uint32_t *__restrict__ heads,
+                                                             const uint32_t *__restrict__ where,
+                                                             const uint16_t *__restrict__ run_start,
+                                                             const uint32_t *__restrict__ run_count,
+                                                             const int32_t *__restrict__ offsets, int E,
+                                                             int32_t *__restrict__ order, int32_t *__restrict__ place) {
+    constexpr int WORDS = RUN_TILE / 32;
+    __shared__ uint32_t word[WORDS], before[WORDS];
+    __shared__ uint32_t shift[RUN_TILE];   // position less place in the tile, of each run
+    __shared__ int32_t out[RUN_TILE];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t0 = (long long)blockIdx.x * RUN_TILE;
+    const int count = (int)min((long long)RUN_TILE, n - t0);
+    const uint32_t runs = run_count[blockIdx.x];
+    for (uint32_t r = threadIdx.x; r < runs; r += THREADS) shift[r] = where[t0 + r] - run_start[t0 + r];
+    if (threadIdx.x < WORDS) word[threadIdx.x] = heads[(size_t)blockIdx.x * WORDS + threadIdx.x];
+    const uint32_t live = (uint32_t)__ldg(offsets + E);  // positions from here on are empty slots
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t c[4], s = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) c[u] = __popc(word[lane * 4 + u]), s += c[u];
+        const uint32_t sum = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        uint32_t b = s - sum;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            before[lane * 4 + u] = b;
+            b += c[u];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < RUN_ITEMS; ++q) {
+        const int p = warp * (32 * RUN_ITEMS) + 32 * q + lane;
+        if (p >= count) continue;
+        const uint32_t r = before[p >> 5] + __popc(word[p >> 5] & (0xffffffffu >> (31 - lane))) - 1;
+        const uint32_t pos = shift[r] + p, i = local[t0 + p];
+        const bool empty = pos >= live;
+        order[pos] = empty ? -1 : (int32_t)(t0 + i);
+        out[i] = empty ? -1 : (int32_t)pos;
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < count; p += THREADS) place[t0 + p] = out[p];
+}
+
+// workspace of the sort by runs
+struct RunSpace {
+    uint32_t *totals, *counts, *base, *run_count, *heads, *sums, *run_key, *list[2][2];
+    uint16_t *local, *run_start;
+    int tiles;
+    size_t bytes;
+    RunSpace(void *ws, long long n, const Plan &p) {
+        tiles = (int)((n + RUN_TILE - 1) / RUN_TILE);
+        const size_t slots = (size_t)tiles * RUN_TILE;
+        char *base_p = static_cast<char *>(ws);
+        size_t at = 0;
+        auto take = [&](size_t b) {
+            char *q = base_p + at;
+            at += up(b);
+            return q;
+        };
+        totals = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) << p.bits));
+        counts = reinterpret_cast<uint32_t *>(take((sizeof(uint32_t) << p.bits) * MAX_BLOCKS));
+        base = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * ((size_t)tiles + 1)));
+        run_count = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * (size_t)tiles));
+        heads = reinterpret_cast<uint32_t *>(take(slots / 8));
+        sums = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * MAX_BLOCKS));
+        run_key = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * slots));
+        for (int g = 0; g < 2; ++g)
+            for (int h = 0; h < 2; ++h) list[g][h] = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * slots));
+        local = reinterpret_cast<uint16_t *>(take(sizeof(uint16_t) * slots));
+        run_start = reinterpret_cast<uint16_t *>(take(sizeof(uint16_t) * slots));
+        bytes = at;
+    }
+};
+
+cudaError_t route_by_runs(const int32_t *ids, long long n, int E, const Plan &p, int32_t *offsets, int32_t *order,
+                          int32_t *place, void *ws, cudaStream_t st) {
+    const RunSpace s(ws, n, p);
+    const int D = 1 << p.bits;
+    const uint32_t *length = s.base + s.tiles;
+    const size_t sort_shared = RUN_TILE * 6 + (size_t)WARPS * D * 2;
+    tile_sort_kernel<<<s.tiles, THREADS, sort_shared, st>>>(ids, n, E, p.passes, p.bits, s.local, s.heads, s.run_key,
+                                                            s.run_start, s.run_count);
+    run_base_kernel<<<1, 1024, 0, st>>>(s.run_count, s.tiles, s.base);
+    run_list_kernel<<<s.tiles, THREADS, 0, st>>>(s.run_key, s.base, s.list[0][0], s.list[0][1]);
+    for (int q = 0; q < p.passes; ++q) {
+        uint32_t *const *from = s.list[q & 1], *const *to = s.list[~q & 1];
+        const long long slots = (long long)s.tiles * RUN_TILE;
+        count_kernel<<<MAX_BLOCKS, THREADS, D * sizeof(uint32_t), st>>>(nullptr, from[0], slots, E, 0, q * p.bits,
+                                                                        p.bits, s.counts, length);
+        scan_kernel<<<D, THREADS, 0, st>>>(s.counts, MAX_BLOCKS, s.totals);
+        move_kernel<<<MAX_BLOCKS, THREADS, (size_t)D * (1 + WARPS) * sizeof(uint32_t), st>>>(
+            nullptr, from[0], from[1], slots, E, 0, q * p.bits, p.bits, s.counts, s.totals, to[0], to[1], nullptr,
+            nullptr, nullptr, length);
+    }
+    uint32_t *const *sorted = s.list[p.passes & 1], *const *spare = s.list[~p.passes & 1];
+    // the keys of the tiles' runs are in the lists: their place takes the positions
+    run_sum_kernel<<<MAX_BLOCKS, THREADS, 0, st>>>(sorted[1], length, s.run_start, s.run_count, n, s.sums);
+    run_place_kernel<<<MAX_BLOCKS, THREADS, 0, st>>>(sorted[1], length, s.run_start, s.run_count, n, s.sums, s.run_key,
+                                                     spare[0]);
+    run_offsets_kernel<<<E / THREADS + 1, THREADS, 0, st>>>(sorted[0], spare[0], length, n, E, offsets);
+    tile_write_kernel<<<s.tiles, THREADS, 0, st>>>(n, s.local, s.heads, s.run_key, s.run_start, s.run_count, offsets,
+                                                   E, order, place);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t route_workspace_bytes(long long n_rows, int K, int E) {
     const long long n = n_rows * K;
     const Plan p = make_plan(n, E);
+    if (p.by_runs) return RunSpace(nullptr, n, p).bytes;
     const size_t table = up(sizeof(uint32_t) << p.bits) + up((sizeof(uint32_t) << p.bits) * p.blocks);
     // keys and pairs between passes, twice when there are two gaps or more
     const size_t lists = p.passes > 1 ? 2 * up(sizeof(uint32_t) * (size_t)n) * (p.passes > 2 ? 2 : 1) : 0;
@@ -229,6 +646,7 @@ cudaError_t launch_route(const int32_t *ids, long long n_rows, int K, int E, int
     const long long n = n_rows * K;
     if (n == 0) return cudaMemsetAsync(offsets, 0, sizeof(int32_t) * ((size_t)E + 1), st);
     const Plan p = make_plan(n, E);
+    if (p.by_runs) return route_by_runs(ids, n, E, p, offsets, order, place, ws, st);
     const int D = 1 << p.bits;
     char *w = static_cast<char *>(ws);
     uint32_t *totals = reinterpret_cast<uint32_t *>(w);
@@ -244,12 +662,12 @@ cudaError_t launch_route(const int32_t *ids, long long n_rows, int K, int E, int
         const bool last = q == p.passes - 1;
         const int shift = q * p.bits;
         count_kernel<<<p.blocks, THREADS, D * sizeof(uint32_t), st>>>(ids, keys, n, E, p.per_block, shift, p.bits,
-                                                                      counts);
+                                                                      counts, nullptr);
         scan_kernel<<<D, THREADS, 0, st>>>(counts, p.blocks, totals);
         uint32_t *ko = last ? nullptr : buf[q & 1][0], *po = last ? nullptr : buf[q & 1][1];
         move_kernel<<<p.blocks, THREADS, (size_t)D * (1 + WARPS) * sizeof(uint32_t), st>>>(
             ids, keys, pairs, n, E, p.per_block, shift, p.bits, counts, totals, ko, po, last ? order : nullptr,
-            last ? place : nullptr, last && p.passes == 1 ? offsets : nullptr);
+            last ? place : nullptr, last && p.passes == 1 ? offsets : nullptr, nullptr);
         keys = ko;
         pairs = po;
     }

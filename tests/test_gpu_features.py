@@ -676,3 +676,34 @@ def test_blend_backward_beyond_the_cache(T, E, D, dt):
     close(dF, ref, torch.minimum(count + 1, torch.tensor(4096.0 + 1100, device="cuda").double()) * U * big)
     dF2, dw2 = f.blend_backward(dout, F, ids, w, r)
     assert torch.equal(dF, dF2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("kind", ["random", "coherent", "one", "none", "sorted", "reversed", "two"])
+@pytest.mark.parametrize("T,K,E", [(131072, 8, 1024), (131073, 8, 5000), (150001, 7, 131072), (1048577, 1, 1 << 20),
+                                   (140000, 8, 1 << 21), (262144, 4, 60000)])
+def test_route_of_many_pairs(T, K, E, kind):
+    """From 2^20 pairs and 1024 sites on the tiles' runs are sorted: the same
+    whole numbers, whatever the runs are."""
+    g = rng(T + E)
+    j = torch.arange(T * K, device="cuda")
+    ids = {"random": lambda: torch.randint(0, E, (T * K,), generator=g, device="cuda"),
+           "coherent": lambda: (j // 40 * 7919 + torch.randint(0, 6, (T * K,), generator=g, device="cuda")) % E,
+           "one": lambda: torch.full_like(j, E - 1), "none": lambda: torch.full_like(j, E + 3),
+           "sorted": lambda: j * E // (T * K), "reversed": lambda: E - 1 - j * E // (T * K),
+           "two": lambda: (j & 1) * (E - 1)}[kind]()
+    if kind in ("random", "coherent"):
+        ids = torch.where(torch.rand(T * K, generator=g, device="cuda") < 0.03, -1, ids)
+    ids = ids.int().view(T, K).contiguous()
+    r = feat().Route(T, K, E)
+    r.workspace.fill_(255)
+    r.build(ids)
+    flat = ids.view(-1).long()
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    skey, perm = torch.sort(key, stable=True)
+    m = int((key < E).sum())
+    pos = torch.arange(T * K, device="cuda")
+    place = torch.empty_like(pos)
+    place[perm] = pos
+    assert torch.equal(r.order.long(), torch.where(pos < m, perm, -1))
+    assert torch.equal(r.place.view(-1).long(), torch.where(key < E, place, -1))
+    assert torch.equal(r.offsets.long(), torch.searchsorted(skey, torch.arange(E + 1, device="cuda")))
