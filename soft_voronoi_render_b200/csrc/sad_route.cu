@@ -42,6 +42,10 @@ struct Plan {
 constexpr int RUN_ITEMS = 16;
 constexpr int RUN_TILE = THREADS * RUN_ITEMS;
 constexpr long long RUN_PAIRS = 1 << 20;
+constexpr int TILE_BITS = 12;      // a place in a tile, or a run's length less 1 ...
+constexpr int RUN_KEY_BITS = 20;   // ... in one word with the key
+static_assert(RUN_TILE == 1 << TILE_BITS && TILE_BITS + RUN_KEY_BITS == 32, "one word a pair");
+constexpr int RUN_BLOCKS = 148 * 8;
 
 Plan make_plan(long long n, int E) {
     int key_bits = 1;
@@ -49,7 +53,7 @@ Plan make_plan(long long n, int E) {
     Plan p;
     p.passes = (key_bits + MAX_BITS - 1) / MAX_BITS;
     p.bits = (key_bits + p.passes - 1) / p.passes;
-    p.by_runs = p.passes > 1 && n >= RUN_PAIRS;
+    p.by_runs = p.passes > 1 && key_bits <= RUN_KEY_BITS && n >= RUN_PAIRS;
     const long long tiles = (n + TILE - 1) / TILE;
     p.blocks = (int)(tiles < MAX_BLOCKS ? (tiles ? tiles : 1) : MAX_BLOCKS);
     const long long tpb = (tiles + p.blocks - 1) / p.blocks;
@@ -245,65 +249,67 @@ __global__ void __launch_bounds__(THREADS) offsets_kernel(const int32_t *__restr
 // ---------------------------------------------------------------------------
 // by runs
 // ---------------------------------------------------------------------------
-// Sorts a tile of pairs by key in shared memory, stable.  Writes the pairs'
-// places in the tile in sorted order (local), a bit for every place where
-// another key starts (heads), and for every run its key and first place; runs
-// of tile t are entries t RUN_TILE + 0, 1, ...
-__global__ void __launch_bounds__(THREADS, 3) tile_sort_kernel(const int32_t *__restrict__ ids, long long n, int E,
-                                                            int passes, int bits, uint16_t *__restrict__ local,
-                                                            uint32_t *__restrict__ heads,
-                                                            uint32_t *__restrict__ run_key,
-                                                            uint16_t *__restrict__ run_start,
-                                                            uint32_t *__restrict__ run_count) {
+// Sorts a tile of pairs by key in shared memory, stable; a pair is one word,
+// key and place in the tile.  Writes the pairs' places in sorted order
+// (local), a bit for every place where another key starts (heads) with the
+// number of such places before each 32 (before), and for every run its first
+// place and its word, key and length less 1; runs of tile t are entries
+// t RUN_TILE + 0, 1, ...
+constexpr int WORDS = RUN_TILE / 32;
+__global__ void __launch_bounds__(THREADS, 4) tile_sort_kernel(const int32_t *__restrict__ ids, long long n, int E,
+                                                               int passes, int bits, uint16_t *__restrict__ local,
+                                                               uint32_t *__restrict__ heads,
+                                                               uint16_t *__restrict__ heads_before,
+                                                               uint32_t *__restrict__ run_word,
+                                                               uint16_t *__restrict__ run_start,
+                                                               uint32_t *__restrict__ run_count) {
     extern __shared__ uint32_t smem[];
     __shared__ uint32_t warp_sum[WARPS];
-    constexpr int WORDS = RUN_TILE / 32;
     __shared__ uint32_t word[WORDS], before[WORDS];
     const int D = 1 << bits;
-    uint32_t *keys = smem;                                            // [RUN_TILE]
-    uint16_t *at = reinterpret_cast<uint16_t *>(smem + RUN_TILE);     // [RUN_TILE]
-    uint16_t *wc = at + RUN_TILE;                                     // [WARPS][D]
+    uint32_t *items = smem;                                           // [RUN_TILE]
+    uint16_t *wc = reinterpret_cast<uint16_t *>(smem + RUN_TILE);     // [WARPS][D]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long t0 = (long long)blockIdx.x * RUN_TILE;
     const int count = (int)min((long long)RUN_TILE, n - t0);
     const int p0 = warp * (32 * RUN_ITEMS) + lane;  // this thread's places: p0 + 32 q
-    uint32_t key[RUN_ITEMS];
-    uint16_t idx[RUN_ITEMS];
+    uint32_t item[RUN_ITEMS];
 #pragma unroll
     for (int q = 0; q < RUN_ITEMS; ++q) {
         const int p = p0 + 32 * q;
-        key[q] = p < count ? key_of(__ldg(ids + t0 + p), E) : 0xffffffffu;
-        idx[q] = (uint16_t)p;
+        // places beyond the last pair have the largest digits and come last, so stay last
+        item[q] = p < count ? key_of(__ldg(ids + t0 + p), E) << TILE_BITS | (uint32_t)p : 0xffffffffu;
     }
     uint16_t *mine = wc + warp * D;
     for (int pass = 0; pass < passes; ++pass) {
-        const int shift = pass * bits;
+        const int shift = TILE_BITS + pass * bits;
         for (int d = lane; d < D / 2; d += 32) reinterpret_cast<uint32_t *>(mine)[d] = 0;
         __syncwarp();
-        uint16_t rank[RUN_ITEMS];
+        uint32_t rank[RUN_ITEMS];
 #pragma unroll
         for (int q = 0; q < RUN_ITEMS; ++q) {
-            // places beyond the last pair have the largest digits and come last, so stay last
-            const uint32_t d = key[q] >> shift & (D - 1);
+            const uint32_t d = item[q] >> shift & (D - 1);
             const unsigned peers = __match_any_sync(0xffffffffu, d);
             const unsigned below = peers & ((1u << lane) - 1);
             const uint32_t old = mine[d];
             __syncwarp();
             if (below == 0) mine[d] = (uint16_t)(old + __popc(peers));
             __syncwarp();
-            rank[q] = (uint16_t)(old + __popc(below));
+            rank[q] = old + __popc(below);
         }
         __syncthreads();
-        // starts of the warps' items: digits in order, warps in order
+        // starts of the warps' items: digits in order, warps in order; a
+        // thread takes 2 digits a step
         uint32_t carry = 0;
-        for (int d0 = 0; d0 < D; d0 += THREADS) {
-            const int d = d0 + threadIdx.x;
-            uint32_t total = 0;
+        for (int d0 = 0; d0 < D; d0 += 2 * THREADS) {
+            const int d = d0 + 2 * threadIdx.x;
+            uint32_t total = 0;  // two counts of 16 bits
             if (d < D) {
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) total += wc[w * D + d];
+                for (int w = 0; w < WARPS; ++w) total += *reinterpret_cast<uint32_t *>(wc + w * D + d);
             }
-            uint32_t s = total;
+            const uint32_t both_d = (total & 0xffffu) + (total >> 16);
+            uint32_t s = both_d;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
@@ -311,42 +317,38 @@ __global__ void __launch_bounds__(THREADS, 3) tile_sort_kernel(const int32_t *__
             }
             if (lane == 31) warp_sum[warp] = s;
             __syncthreads();
-            uint32_t start = carry + s - total;
+            uint32_t start = carry + s - both_d;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
                 if (w < warp) start += warp_sum[w];
                 carry += warp_sum[w];
             }
             if (d < D) {
+                // both starts are at most 4096
+                uint32_t at = start | (start + (total & 0xffffu)) << 16;
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
-                    const uint32_t c = wc[w * D + d];
-                    wc[w * D + d] = (uint16_t)start;
-                    start += c;
+                    uint32_t *c = reinterpret_cast<uint32_t *>(wc + w * D + d);
+                    const uint32_t add = *c;
+                    *c = at;
+                    at += add;
                 }
             }
             __syncthreads();
         }
 #pragma unroll
-        for (int q = 0; q < RUN_ITEMS; ++q) {
-            const int to = mine[key[q] >> shift & (D - 1)] + rank[q];
-            keys[to] = key[q];
-            at[to] = idx[q];
-        }
+        for (int q = 0; q < RUN_ITEMS; ++q) items[mine[item[q] >> shift & (D - 1)] + rank[q]] = item[q];
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < RUN_ITEMS; ++q) {
-            key[q] = keys[p0 + 32 * q];
-            idx[q] = at[p0 + 32 * q];
-        }
+        for (int q = 0; q < RUN_ITEMS; ++q) item[q] = items[p0 + 32 * q];
     }
 #pragma unroll
     for (int q = 0; q < RUN_ITEMS; ++q) {
         const int p = p0 + 32 * q;
-        const bool head = p < count && (p == 0 || keys[p - 1] != key[q]);
+        const bool head = p < count && (p == 0 || (items[p - 1] ^ item[q]) >> TILE_BITS);
         const uint32_t b = __ballot_sync(0xffffffffu, head);
         if (lane == 0) word[p >> 5] = b;
-        if (p < count) local[t0 + p] = idx[q];
+        if (p < count) local[t0 + p] = (uint16_t)(item[q] & (RUN_TILE - 1));
     }
     __syncthreads();
     static_assert(WORDS == 4 * 32, "one warp scans four words a lane");
@@ -368,15 +370,30 @@ __global__ void __launch_bounds__(THREADS, 3) tile_sort_kernel(const int32_t *__
         }
         if (lane == 31) run_count[blockIdx.x] = s;
     }
-    if (threadIdx.x < WORDS) heads[(size_t)blockIdx.x * WORDS + threadIdx.x] = word[threadIdx.x];
     __syncthreads();
+    if (threadIdx.x < WORDS) {
+        heads[(size_t)blockIdx.x * WORDS + threadIdx.x] = word[threadIdx.x];
+        heads_before[(size_t)blockIdx.x * WORDS + threadIdx.x] = (uint16_t)before[threadIdx.x];
+    }
 #pragma unroll
     for (int q = 0; q < RUN_ITEMS; ++q) {
         const int p = p0 + 32 * q;
         const uint32_t b = word[p >> 5];
         if (!(b >> lane & 1u)) continue;
         const uint32_t r = before[p >> 5] + __popc(b & ((1u << lane) - 1));
-        run_key[t0 + r] = key[q];
+        // the next head, in this word or a later one
+        const uint32_t rest = lane < 31 ? b >> (lane + 1) : 0;
+        int end = count;
+        if (rest) {
+            end = p + __ffs(rest);
+        } else {
+            for (int v = (p >> 5) + 1; v < WORDS; ++v)
+                if (word[v]) {
+                    end = v * 32 + __ffs(word[v]) - 1;
+                    break;
+                }
+        }
+        run_word[t0 + r] = (item[q] & ~(uint32_t)(RUN_TILE - 1)) | (uint32_t)(end - p - 1);
         run_start[t0 + r] = (uint16_t)p;
     }
 }
@@ -384,13 +401,18 @@ __global__ void __launch_bounds__(THREADS, 3) tile_sort_kernel(const int32_t *__
 // base[t] = runs of the tiles before t; base[tiles] = all
 __global__ void __launch_bounds__(1024) run_base_kernel(const uint32_t *__restrict__ run_count, int tiles,
                                                         uint32_t *__restrict__ base) {
+    constexpr int EACH = 8;
     __shared__ uint32_t warp_sum[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t carry = 0;
-    for (int t0 = 0; t0 < tiles; t0 += 1024) {
-        const int t = t0 + threadIdx.x;
-        const uint32_t v = t < tiles ? run_count[t] : 0;
-        uint32_t s = v;
+    for (int t0 = 0; t0 < tiles; t0 += 1024 * EACH) {
+        const int t = t0 + threadIdx.x * EACH;
+        uint32_t v[EACH], sum = 0;
+#pragma unroll
+        for (int u = 0; u < EACH; ++u) v[u] = t + u < tiles ? run_count[t + u] : 0;
+#pragma unroll
+        for (int u = 0; u < EACH; ++u) sum += v[u];
+        uint32_t s = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
@@ -398,51 +420,51 @@ __global__ void __launch_bounds__(1024) run_base_kernel(const uint32_t *__restri
         }
         if (lane == 31) warp_sum[warp] = s;
         __syncthreads();
-        uint32_t start = carry + s - v;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) start += warp_sum[w];
-            carry += warp_sum[w];
+        uint32_t ws = warp_sum[lane];
+        const uint32_t own = ws;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, ws, o);
+            if (lane >= o) ws += u;
         }
-        if (t < tiles) base[t] = start;
+        uint32_t start = carry + s - sum + __shfl_sync(0xffffffffu, ws - own, warp);
+        carry += __shfl_sync(0xffffffffu, ws, 31);
+#pragma unroll
+        for (int u = 0; u < EACH; ++u) {
+            if (t + u < tiles) base[t + u] = start;
+            start += v[u];
+        }
         __syncthreads();
     }
     if (threadIdx.x == 0) base[tiles] = carry;
 }
 
-// the runs of all tiles behind one another: key, and the run's entry
-__global__ void __launch_bounds__(THREADS) run_list_kernel(const uint32_t *__restrict__ run_key,
+// the runs of all tiles behind one another: word, and the run's entry
+__global__ void __launch_bounds__(THREADS) run_list_kernel(const uint32_t *__restrict__ run_word,
                                                            const uint32_t *__restrict__ base,
-                                                           uint32_t *__restrict__ key, uint32_t *__restrict__ entry) {
+                                                           uint32_t *__restrict__ word, uint32_t *__restrict__ entry) {
     const uint32_t from = base[blockIdx.x], count = base[blockIdx.x + 1] - from;
     const uint32_t t0 = blockIdx.x * (uint32_t)RUN_TILE;
     for (uint32_t r = threadIdx.x; r < count; r += THREADS) {
-        key[from + r] = run_key[t0 + r];
+        word[from + r] = run_word[t0 + r];
         entry[from + r] = t0 + r;
     }
 }
 
-// pairs in the run of an entry
-__device__ __forceinline__ uint32_t run_length(uint32_t entry, const uint16_t *__restrict__ run_start,
-                                               const uint32_t *__restrict__ run_count, long long n) {
-    const uint32_t t = entry / RUN_TILE, r = entry % RUN_TILE;
-    const uint32_t end = r + 1 < run_count[t] ? run_start[entry + 1]
-                                              : (uint32_t)min((long long)RUN_TILE, n - (long long)t * RUN_TILE);
-    return end - run_start[entry];
-}
+// pairs of a run, from its word
+__device__ __forceinline__ uint32_t run_length(uint32_t word) { return (word & (RUN_TILE - 1)) + 1; }
 
 // The sorted runs' first positions: a run of runs a block, its sum first,
 // then its scan behind the sums of the blocks before it.  where[entry] is the
 // position for the tiles, sorted[i] the same by rank for the offsets.
-__global__ void __launch_bounds__(THREADS) run_sum_kernel(const uint32_t *__restrict__ entry,
+__global__ void __launch_bounds__(THREADS) run_sum_kernel(const uint32_t *__restrict__ word,
                                                           const uint32_t *__restrict__ length,
-                                                          const uint16_t *__restrict__ run_start,
-                                                          const uint32_t *__restrict__ run_count, long long n,
                                                           uint32_t *__restrict__ sums) {
     __shared__ uint32_t warp_sum[WARPS];
     const uint32_t total = *length, each = (total + gridDim.x - 1) / gridDim.x;
     const uint32_t lo = min(blockIdx.x * each, total), hi = min(lo + each, total);
     uint32_t s = 0;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += THREADS) s += run_length(entry[i], run_start, run_count, n);
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += THREADS) s += run_length(word[i]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
@@ -453,10 +475,9 @@ __global__ void __launch_bounds__(THREADS) run_sum_kernel(const uint32_t *__rest
         sums[blockIdx.x] = s;
     }
 }
-__global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__restrict__ entry,
+__global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__restrict__ word,
+                                                            const uint32_t *__restrict__ entry,
                                                             const uint32_t *__restrict__ length,
-                                                            const uint16_t *__restrict__ run_start,
-                                                            const uint32_t *__restrict__ run_count, long long n,
                                                             const uint32_t *__restrict__ sums,
                                                             uint32_t *__restrict__ where,
                                                             uint32_t *__restrict__ sorted) {
@@ -475,7 +496,7 @@ __global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__re
     __syncthreads();
     for (uint32_t i0 = lo; i0 < hi; i0 += THREADS) {
         const uint32_t i = i0 + threadIdx.x;
-        const uint32_t e = i < hi ? entry[i] : 0, v = i < hi ? run_length(e, run_start, run_count, n) : 0;
+        const uint32_t e = i < hi ? entry[i] : 0, v = i < hi ? run_length(word[i]) : 0;
         uint32_t s = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -499,7 +520,7 @@ __global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__re
 }
 
 // offsets[e]: the first position of the first run with a key of e or more
-__global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__restrict__ key,
+__global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__restrict__ word,
                                                               const uint32_t *__restrict__ sorted,
                                                               const uint32_t *__restrict__ length, long long n, int E,
                                                               int32_t *__restrict__ offsets) {
@@ -509,7 +530,7 @@ __global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__
     uint32_t lo = 0, hi = total;
     while (lo < hi) {
         const uint32_t mid = (lo + hi) >> 1;
-        if (__ldg(key + mid) < (uint32_t)e) lo = mid + 1;
+        if (__ldg(word + mid) >> TILE_BITS < (uint32_t)e) lo = mid + 1;
         else hi = mid;
     }
     offsets[e] = (int32_t)(lo < total ? sorted[lo] : (uint32_t)n);
@@ -518,50 +539,39 @@ __global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__
 // a tile's part of order and place
 __global__ void __launch_bounds__(THREADS) tile_write_kernel(long long n, const uint16_t *__restrict__ local,
                                                              const uint32_t *__restrict__ heads,
+                                                             const uint16_t *__restrict__ heads_before,
                                                              const uint32_t *__restrict__ where,
                                                              const uint16_t *__restrict__ run_start,
                                                              const uint32_t *__restrict__ run_count,
                                                              const int32_t *__restrict__ offsets, int E,
                                                              int32_t *__restrict__ order, int32_t *__restrict__ place) {
-    constexpr int WORDS = RUN_TILE / 32;
-    __shared__ uint32_t word[WORDS], before[WORDS];
     __shared__ uint32_t shift[RUN_TILE];   // position less place in the tile, of each run
     __shared__ int32_t out[RUN_TILE];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long t0 = (long long)blockIdx.x * RUN_TILE;
     const int count = (int)min((long long)RUN_TILE, n - t0);
     const uint32_t runs = run_count[blockIdx.x];
-    for (uint32_t r = threadIdx.x; r < runs; r += THREADS) shift[r] = where[t0 + r] - run_start[t0 + r];
-    if (threadIdx.x < WORDS) word[threadIdx.x] = heads[(size_t)blockIdx.x * WORDS + threadIdx.x];
-    const uint32_t live = (uint32_t)__ldg(offsets + E);  // positions from here on are empty slots
-    __syncthreads();
-    if (warp == 0) {
-        uint32_t c[4], s = 0;
+    // everything is loaded before the first wait
+    uint16_t idx[RUN_ITEMS];
+    uint32_t word[RUN_ITEMS], before[RUN_ITEMS];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) c[u] = __popc(word[lane * 4 + u]), s += c[u];
-        const uint32_t sum = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += u;
-        }
-        uint32_t b = s - sum;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            before[lane * 4 + u] = b;
-            b += c[u];
-        }
+    for (int q = 0; q < RUN_ITEMS; ++q) {
+        const int w = warp * RUN_ITEMS + q, p = 32 * w + lane;
+        idx[q] = p < count ? local[t0 + p] : 0;
+        word[q] = __ldg(heads + (size_t)blockIdx.x * WORDS + w);
+        before[q] = __ldg(heads_before + (size_t)blockIdx.x * WORDS + w);
     }
+    const uint32_t live = (uint32_t)__ldg(offsets + E);  // positions from here on are empty slots
+    for (uint32_t r = threadIdx.x; r < runs; r += THREADS) shift[r] = where[t0 + r] - run_start[t0 + r];
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < RUN_ITEMS; ++q) {
         const int p = warp * (32 * RUN_ITEMS) + 32 * q + lane;
         if (p >= count) continue;
-        const uint32_t r = before[p >> 5] + __popc(word[p >> 5] & (0xffffffffu >> (31 - lane))) - 1;
-        const uint32_t pos = shift[r] + p, i = local[t0 + p];
+        const uint32_t pos = shift[before[q] + __popc(word[q] & (0xffffffffu >> (31 - lane))) - 1] + p;
         const bool empty = pos >= live;
-        order[pos] = empty ? -1 : (int32_t)(t0 + i);
-        out[i] = empty ? -1 : (int32_t)pos;
+        order[pos] = empty ? -1 : (int32_t)(t0 + idx[q]);
+        out[idx[q]] = empty ? -1 : (int32_t)pos;
     }
     __syncthreads();
     for (int p = threadIdx.x; p < count; p += THREADS) place[t0 + p] = out[p];
@@ -569,8 +579,8 @@ __global__ void __launch_bounds__(THREADS) tile_write_kernel(long long n, const 
 
 // workspace of the sort by runs
 struct RunSpace {
-    uint32_t *totals, *counts, *base, *run_count, *heads, *sums, *run_key, *list[2][2];
-    uint16_t *local, *run_start;
+    uint32_t *totals, *counts, *base, *run_count, *heads, *sums, *run_word, *list[2][2];
+    uint16_t *local, *run_start, *heads_before;
     int tiles;
     size_t bytes;
     RunSpace(void *ws, long long n, const Plan &p) {
@@ -584,12 +594,13 @@ struct RunSpace {
             return q;
         };
         totals = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) << p.bits));
-        counts = reinterpret_cast<uint32_t *>(take((sizeof(uint32_t) << p.bits) * MAX_BLOCKS));
+        counts = reinterpret_cast<uint32_t *>(take((sizeof(uint32_t) << p.bits) * RUN_BLOCKS));
         base = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * ((size_t)tiles + 1)));
         run_count = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * (size_t)tiles));
         heads = reinterpret_cast<uint32_t *>(take(slots / 8));
-        sums = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * MAX_BLOCKS));
-        run_key = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * slots));
+        sums = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * RUN_BLOCKS));
+        heads_before = reinterpret_cast<uint16_t *>(take(slots / 16));
+        run_word = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * slots));
         for (int g = 0; g < 2; ++g)
             for (int h = 0; h < 2; ++h) list[g][h] = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * slots));
         local = reinterpret_cast<uint16_t *>(take(sizeof(uint16_t) * slots));
@@ -603,29 +614,29 @@ cudaError_t route_by_runs(const int32_t *ids, long long n, int E, const Plan &p,
     const RunSpace s(ws, n, p);
     const int D = 1 << p.bits;
     const uint32_t *length = s.base + s.tiles;
-    const size_t sort_shared = RUN_TILE * 6 + (size_t)WARPS * D * 2;
-    tile_sort_kernel<<<s.tiles, THREADS, sort_shared, st>>>(ids, n, E, p.passes, p.bits, s.local, s.heads, s.run_key,
-                                                            s.run_start, s.run_count);
+    const size_t sort_shared = RUN_TILE * sizeof(uint32_t) + (size_t)WARPS * D * sizeof(uint16_t);
+    tile_sort_kernel<<<s.tiles, THREADS, sort_shared, st>>>(ids, n, E, p.passes, p.bits, s.local, s.heads,
+                                                            s.heads_before, s.run_word, s.run_start, s.run_count);
     run_base_kernel<<<1, 1024, 0, st>>>(s.run_count, s.tiles, s.base);
-    run_list_kernel<<<s.tiles, THREADS, 0, st>>>(s.run_key, s.base, s.list[0][0], s.list[0][1]);
+    run_list_kernel<<<s.tiles, THREADS, 0, st>>>(s.run_word, s.base, s.list[0][0], s.list[0][1]);
     for (int q = 0; q < p.passes; ++q) {
         uint32_t *const *from = s.list[q & 1], *const *to = s.list[~q & 1];
         const long long slots = (long long)s.tiles * RUN_TILE;
-        count_kernel<<<MAX_BLOCKS, THREADS, D * sizeof(uint32_t), st>>>(nullptr, from[0], slots, E, 0, q * p.bits,
-                                                                        p.bits, s.counts, length);
-        scan_kernel<<<D, THREADS, 0, st>>>(s.counts, MAX_BLOCKS, s.totals);
-        move_kernel<<<MAX_BLOCKS, THREADS, (size_t)D * (1 + WARPS) * sizeof(uint32_t), st>>>(
-            nullptr, from[0], from[1], slots, E, 0, q * p.bits, p.bits, s.counts, s.totals, to[0], to[1], nullptr,
-            nullptr, nullptr, length);
+        const int shift = TILE_BITS + q * p.bits;
+        count_kernel<<<RUN_BLOCKS, THREADS, D * sizeof(uint32_t), st>>>(nullptr, from[0], slots, E, 0, shift, p.bits,
+                                                                        s.counts, length);
+        scan_kernel<<<D, THREADS, 0, st>>>(s.counts, RUN_BLOCKS, s.totals);
+        move_kernel<<<RUN_BLOCKS, THREADS, (size_t)D * (1 + WARPS) * sizeof(uint32_t), st>>>(
+            nullptr, from[0], from[1], slots, E, 0, shift, p.bits, s.counts, s.totals, to[0], to[1], nullptr, nullptr,
+            nullptr, length);
     }
     uint32_t *const *sorted = s.list[p.passes & 1], *const *spare = s.list[~p.passes & 1];
-    // the keys of the tiles' runs are in the lists: their place takes the positions
-    run_sum_kernel<<<MAX_BLOCKS, THREADS, 0, st>>>(sorted[1], length, s.run_start, s.run_count, n, s.sums);
-    run_place_kernel<<<MAX_BLOCKS, THREADS, 0, st>>>(sorted[1], length, s.run_start, s.run_count, n, s.sums, s.run_key,
-                                                     spare[0]);
+    // the words of the tiles' runs are in the lists: their place takes the positions
+    run_sum_kernel<<<RUN_BLOCKS, THREADS, 0, st>>>(sorted[0], length, s.sums);
+    run_place_kernel<<<RUN_BLOCKS, THREADS, 0, st>>>(sorted[0], sorted[1], length, s.sums, s.run_word, spare[0]);
     run_offsets_kernel<<<E / THREADS + 1, THREADS, 0, st>>>(sorted[0], spare[0], length, n, E, offsets);
-    tile_write_kernel<<<s.tiles, THREADS, 0, st>>>(n, s.local, s.heads, s.run_key, s.run_start, s.run_count, offsets,
-                                                   E, order, place);
+    tile_write_kernel<<<s.tiles, THREADS, 0, st>>>(n, s.local, s.heads, s.heads_before, s.run_word, s.run_start,
+                                                   s.run_count, offsets, E, order, place);
     return cudaGetLastError();
 }
 
