@@ -16,10 +16,15 @@
 // products are summed over the group by halving: each step of the butterfly
 // also halves the number of sums a lane keeps, 7 + log2(L / 8) shuffles
 // instead of 8 log2 L.
+#include <algorithm>
+
 #include "sad_features.h"
 #include "sad_rows.cuh"
 
 namespace sad {
+
+using std::max;
+using std::min;
 
 namespace {
 
@@ -258,20 +263,84 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
 // ---------------------------------------------------------------------------
 // segment sums
 //
-// The sorted pairs are cut into chunks of C positions, a warp each, whatever
-// the experts' shares are.  A warp walks its chunk's runs of one expert: 32
-// pairs and weights a step, the rows by S = 32 / L groups side by side, and
-// joins the groups at the run's end.  A run that is all of its expert's pairs
-// goes to dF; one that is cut at the chunk's start or end goes to one of the
-// chunk's two partial rows, which join_kernel adds up in order.
+// Near rows (dout within half of the L2): the sorted pairs are cut into chunks
+// of C positions, a warp each, whatever the experts' shares are.  A warp walks
+// its chunk's runs of one expert; a run that is all of its expert's pairs goes
+// to dF, one that is cut at the chunk's start or end to one of the chunk's two
+// partial rows, which join_kernel adds up in order.
 //
-// Every row of dout is read once for each of its K pairs.  Where dout does
-// not fit the L2 and ids are in no order over the rows (sites over an image),
-// chunks side by side in the list would read it from memory eight times
-// (3.2 GB for 2048 x 2048 x 32 bf16, 784 us): the chunks are then taken in
-// the order of their first pair's row, counted into BUCKETS parts of the
-// rows.  The order within a part is not fixed, and no result depends on it.
+// Far rows: every row of dout is read once for each of its K pairs, and where
+// ids are in no order over the rows (sites over an image) experts side by
+// side in the list would read it from memory K times.  So the work is cut at
+// the experts, in pieces of at most C positions, and the pieces are taken in
+// the order of their first pair's row, counted into BUCKETS parts of the rows
+// (2048 x 2048 x 32 bf16: 784 us for 3.2 GB by chunks in their own order, 588
+// us for 1.9 GB with chunks, cut anywhere, in the order of the rows).  The
+// order within a part is not fixed, and no result depends on it.
 // ---------------------------------------------------------------------------
+
+// acc[] = sum of w_j G[j / K] over the sorted positions a ... b - 1, columns c
+// ... of the group: 32 pairs a step, their rows by 32 / L groups side by side.
+// The ids of the pairs two steps ahead and the weights of the next are loaded
+// while the rows of a step are on their way.
+template <typename T, int VEC>
+__device__ __forceinline__ void sum_run(const T *__restrict__ G, uint32_t ldg, const float *__restrict__ w,
+                                        const int32_t *__restrict__ order, uint32_t n, uint32_t K, uint32_t a,
+                                        uint32_t b, int c, bool col, int log_l, float (&acc)[VEC + 1]) {
+    const int L = 1 << log_l, S = 32 >> log_l;
+    const int lane = threadIdx.x & 31, sub = lane >> log_l;
+    Two acc2[(VEC + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i) acc2[i] = two(0.0f, 0.0f);
+    auto pair_at = [&](uint32_t s) { return s + lane < b ? (uint32_t)__ldg(order + s + lane) : 0xffffffffu; };
+    auto weight_of = [&](uint32_t j) { return j < n ? __ldg(w + j) : 0.0f; };
+    uint32_t j = pair_at(a), j_next = pair_at(a + 32);
+    float wj = weight_of(j);
+    for (uint32_t s = a; s < b; s += 32) {
+        const uint32_t row = j < n ? j / K : 0;
+        const uint32_t left = min(b - s, 32u);
+        const uint32_t j_ahead = pair_at(s + 64);
+        float w_next = 0.0f;
+        for (uint32_t q = 0; q < left; q += 4 * S) {
+            Pack<T, VEC> p[4];
+            float wq[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t at = q + u * S + sub;
+                const uint32_t r = __shfl_sync(0xffffffffu, row, at & 31);
+                wq[u] = __shfl_sync(0xffffffffu, wj, at & 31);
+                p[u].clear();
+                if (at < left && col) p[u] = load_pack<T, VEC>(at_row(G, r, ldg, c));
+            }
+            if (q == 0) w_next = weight_of(j_next);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add_scaled(p[u], wq[u], acc2);  // 0 beyond the run
+        }
+        j = j_next;
+        wj = w_next;
+        j_next = j_ahead;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) both(acc2[i / 2], acc[i], acc[i + 1]);
+    for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    }
+}
+
+// to[i] = acc[i], by the first group; `to` may start anywhere on 4 bytes
+template <int VEC> __device__ __forceinline__ void store_sums(float *to, const float (&acc)[VEC + 1]) {
+    constexpr int W = VEC % 4 ? VEC : 4;
+#pragma unroll
+    for (int i = 0; i < VEC; i += W) {
+        Pack<float, W> f;
+#pragma unroll
+        for (int v = 0; v < W; ++v) f.v[v] = acc[i + v];
+        if (W == 4 && (reinterpret_cast<uintptr_t>(to + i) & 15) == 0) store_pack<float, W>(to + i, f);
+        else
+            for (int v = 0; v < W; ++v) to[i + v] = f.v[v];
+    }
+}
 
 // the last e in [0, E) with offsets[e] <= s, for s below offsets[E]
 __device__ __forceinline__ int expert_at(const int32_t *__restrict__ offsets, int E, uint32_t s) {
@@ -285,19 +354,16 @@ __device__ __forceinline__ int expert_at(const int32_t *__restrict__ offsets, in
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ G, uint32_t ldg,
-                                                          const float *__restrict__ w,
-                                                          const int32_t *__restrict__ offsets,
-                                                          const int32_t *__restrict__ order, uint32_t n, int K, int E,
-                                                          int D, int log_l, uint32_t C, uint32_t chunks,
-                                                          const uint32_t *__restrict__ turn,
-                                                          float *__restrict__ dF, float *__restrict__ partial,
-                                                          int32_t *__restrict__ cut_expert) {
-    const int L = 1 << log_l, S = 32 >> log_l;
-    const int lane = threadIdx.x & 31, sub = lane >> log_l, in_row = lane & (L - 1);
-    uint32_t chunk = (uint32_t)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
+__global__ void __launch_bounds__(THREADS, 4) chunk_kernel(const T *__restrict__ G, uint32_t ldg,
+                                                        const float *__restrict__ w,
+                                                        const int32_t *__restrict__ offsets,
+                                                        const int32_t *__restrict__ order, uint32_t n, int K, int E,
+                                                        int D, int log_l, uint32_t C, uint32_t chunks,
+                                                        float *__restrict__ dF, float *__restrict__ partial,
+                                                        int32_t *__restrict__ cut_expert) {
+    const int lane = threadIdx.x & 31, in_row = lane & ((1 << log_l) - 1);
+    const uint32_t chunk = (uint32_t)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
     if (chunk >= chunks) return;
-    if (turn) chunk = min(__ldg(turn + chunk), chunks - 1);
     const uint32_t total = min((uint32_t)__ldg(offsets + E), n);
     const uint32_t lo = chunk * C;
     if (lane == 0 && blockIdx.y == 0) cut_expert[chunk] = -1;
@@ -316,71 +382,60 @@ __global__ void __launch_bounds__(THREADS) segment_kernel(const T *__restrict__ 
                 continue;
             }
             const uint32_t b = min(end, hi);
-            Two acc2[(VEC + 1) / 2];
-#pragma unroll
-            for (int i = 0; i < (VEC + 1) / 2; ++i) acc2[i] = two(0.0f, 0.0f);
-            for (uint32_t s = a; s < b; s += 32) {
-                uint32_t row = 0;
-                float wj = 0.0f;
-                if (s + lane < b) {
-                    const uint32_t j = (uint32_t)__ldg(order + s + lane);
-                    if (j < n) {
-                        row = j / (uint32_t)K;
-                        wj = __ldg(w + j);
-                    }
-                }
-                const uint32_t left = min(b - s, 32u);
-                for (uint32_t q = 0; q < left; q += 4 * S) {
-                    Pack<T, VEC> p[4];
-                    float wq[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t at = q + u * S + sub;
-                        const uint32_t r = __shfl_sync(0xffffffffu, row, at & 31);
-                        wq[u] = __shfl_sync(0xffffffffu, wj, at & 31);
-                        p[u].clear();
-                    if (at < left && col) p[u] = load_pack<T, VEC>(at_row(G, r, ldg, c));
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) add_scaled(p[u], wq[u], acc2);  // 0 beyond the run
-                }
-            }
             float acc[VEC + 1];
-#pragma unroll
-            for (int i = 0; i < VEC; i += 2) both(acc2[i / 2], acc[i], acc[i + 1]);
-            for (int o = L; o < 32; o <<= 1) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-            }
-            if (sub == 0 && col) {
-                const uint32_t from = (uint32_t)__ldg(offsets + e);
-                const bool whole = from == a && end == b;
-                // the expert that starts in this chunk and goes on behind it
-                if (lane == 0 && slab == 0 && from >= lo && end > b) cut_expert[chunk] = e;
-                float *to = whole ? dF + (long long)e * D + c
-                                  : partial + ((size_t)2 * chunk + (a == lo ? 0 : 1)) * D + c;
-                Pack<float, VEC % 4 ? VEC : 4> f;
-                constexpr int FV = VEC % 4 ? VEC : 4;
-#pragma unroll
-                for (int i = 0; i < VEC; i += FV) {
-#pragma unroll
-                    for (int v = 0; v < FV; ++v) f.v[v] = acc[i + v];
-                    // dF may start anywhere on 4 bytes
-                    if (FV == 4 && (reinterpret_cast<uintptr_t>(to + i) & 15) == 0) store_pack<float, FV>(to + i, f);
-                    else
-                        for (int v = 0; v < FV; ++v) to[i + v] = f.v[v];
-                }
-            }
+            sum_run<T, VEC>(G, ldg, w, order, n, (uint32_t)K, a, b, c, col, log_l, acc);
+            const uint32_t from = (uint32_t)__ldg(offsets + e);
+            const bool whole = from == a && end == b;
+            // the expert that starts in this chunk and goes on behind it
+            if (lane == 0 && slab == 0 && from >= lo && end > b) cut_expert[chunk] = e;
+            if (lane >> log_l == 0 && col)
+                store_sums<VEC>(whole ? dF + (long long)e * D + c
+                                      : partial + ((size_t)2 * chunk + (a == lo ? 0 : 1)) * D + c,
+                                acc);
             a = b;
             ++e;
         }
     }
 }
 
+// Sums rows(q), q = from ... last, of D columns into to[]: by one warp, or
+// (many rows) by all warps of the block, a run of the rows each.
+template <typename F>
+__device__ __forceinline__ void sum_rows_warp(F row, uint32_t from, uint32_t last, int D, float *__restrict__ to) {
+    for (int c = threadIdx.x & 31; c < D; c += 32) {
+        float s = 0.0f;
+#pragma unroll 4
+        for (uint32_t q = from; q <= last; ++q) s += __ldg(row(q) + c);
+        to[c] = s;
+    }
+}
+template <typename F>
+__device__ __forceinline__ void sum_rows_block(F row, uint32_t from, uint32_t last, int D, float *__restrict__ to,
+                                               float (*part)[33]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t each = (last - from + WARPS) / WARPS, q0 = from + warp * each, q1 = min(q0 + each, last + 1);
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        const int c = c0 + lane;
+        float s = 0.0f;
+        if (c < D) {
+#pragma unroll 8
+            for (uint32_t q = q0; q < q1; ++q) s += __ldg(row(q) + c);
+        }
+        part[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && c < D) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < WARPS; ++q) sum += part[q][lane];
+            to[c] = sum;
+        }
+        __syncthreads();
+    }
+}
+
 // For each chunk's expert that starts in it and goes on behind it: the sum of
 // that expert's partial rows, from this chunk's to the one that it ends in.
-// A warp a chunk; experts of more than LONG chunks are left to the block,
-// whose warps take a run of the rows each.
+// A warp a chunk; experts of more than LONG chunks are left to the block.
 constexpr uint32_t LONG = 32;
 __global__ void __launch_bounds__(THREADS) join_kernel(const int32_t *__restrict__ offsets,
                                                        const int32_t *__restrict__ cut_expert, uint32_t n, int E,
@@ -396,61 +451,65 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const int32_t *__restrict
         last = min((end - 1) / C, chunks - 1);
         slot = (uint32_t)__ldg(offsets + e) != chunk * C;  // where its first run was put
     };
-    auto row = [&](uint32_t q, uint32_t chunk, int slot) {
-        return partial + ((size_t)2 * q + (q == chunk ? slot : 0)) * D;
-    };
     const uint32_t chunk = blockIdx.x * WARPS + warp;
     int e = -1, slot = 0;
     uint32_t last = 0;
     if (chunk < chunks) span(chunk, e, last, slot);
     const bool later = e >= 0 && last - chunk >= LONG;
     if (lane == 0) long_chunk[warp] = later ? chunk : 0xffffffffu;
-    if (e >= 0 && !later) {
-        for (int c = lane; c < D; c += 32) {
-            float s = 0.0f;
-#pragma unroll 4
-            for (uint32_t q = chunk; q <= last; ++q) s += __ldg(row(q, chunk, slot) + c);
-            dF[(long long)e * D + c] = s;
-        }
-    }
+    auto row = [&](uint32_t q) { return partial + ((size_t)2 * q + (q == chunk ? slot : 0)) * D; };
+    if (e >= 0 && !later) sum_rows_warp(row, chunk, last, D, dF + (long long)e * D);
     __syncthreads();
     for (int k = 0; k < WARPS; ++k) {
         const uint32_t from = long_chunk[k];
         if (from == 0xffffffffu) continue;
         span(from, e, last, slot);
-        const uint32_t each = (last - from + WARPS) / WARPS, q0 = from + warp * each, q1 = min(q0 + each, last + 1);
-        for (int c0 = 0; c0 < D; c0 += 32) {
-            const int c = c0 + lane;
-            float s = 0.0f;
-            if (c < D) {
-#pragma unroll 8
-                for (uint32_t q = q0; q < q1; ++q) s += __ldg(row(q, from, slot) + c);
-            }
-            part[warp][lane] = s;
-            __syncthreads();
-            if (warp == 0 && c < D) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int q = 0; q < WARPS; ++q) sum += part[q][lane];
-                dF[(long long)e * D + c] = sum;
-            }
-            __syncthreads();
-        }
+        auto row_of = [&](uint32_t q) { return partial + ((size_t)2 * q + (q == from ? slot : 0)) * D; };
+        sum_rows_block(row_of, from, last, D, dF + (long long)e * D, part);
     }
 }
 
-// the order in which chunks are taken: a count of each part of the rows, its
-// scan, and the chunks put into their part's places
+// Far rows: pieces of at most C positions of one expert.  Piece k of an expert
+// of several has partial row 2 (from / C) + 1 for k = 0 and 2 (from / C + k)
+// else: experts of more than C positions are more than C apart, so no two
+// share a row.
+__device__ __forceinline__ size_t piece_row(uint32_t from, uint32_t k, uint32_t C) {
+    return k ? 2 * ((size_t)(from / C) + k) : 2 * (size_t)(from / C) + 1;
+}
+
+// The order in which pieces are taken: a count of each part of the rows, its
+// scan, and the pieces put into their part's places.  `per` experts a block:
+// fewer where few experts have many pieces.
 constexpr int BUCKETS = 4096;
-__device__ __forceinline__ uint32_t bucket_of(const int32_t *__restrict__ order, uint32_t chunk, uint32_t C, uint32_t n) {
-    const uint32_t j = (uint32_t)__ldg(order + (size_t)chunk * C);
-    return j < n ? (uint32_t)((unsigned long long)j * BUCKETS / n) : BUCKETS - 1;  // behind the last pair: last
+template <bool PLACE>
+__global__ void __launch_bounds__(THREADS) turn_kernel(const int32_t *__restrict__ offsets,
+                                                       const int32_t *__restrict__ order, uint32_t n, int E, int per,
+                                                       uint32_t C, uint32_t *__restrict__ count, uint32_t most,
+                                                       uint2 *__restrict__ turn) {
+    // a thread takes an expert, and all of them share those of many pieces
+    __shared__ uint32_t s_from[THREADS], s_pieces[THREADS];
+    const long long e0 = (long long)blockIdx.x * per, e = e0 + threadIdx.x;
+    uint32_t from = 0, pieces = 0;
+    if (threadIdx.x < per && e < E) {
+        from = min((uint32_t)__ldg(offsets + e), n);
+        pieces = (min((uint32_t)__ldg(offsets + e + 1), n) - from + C - 1) / C;
+    }
+    auto put = [&](uint32_t expert, uint32_t a, uint32_t k) {
+        const uint32_t at = a + k * C;
+        if (at >= n) return;
+        const uint32_t j = (uint32_t)__ldg(order + at);
+        const uint32_t b = j < n ? (uint32_t)((unsigned long long)j * BUCKETS / n) : BUCKETS - 1;
+        const uint32_t t = atomicAdd(count + b, 1u);
+        if (PLACE && t < most) turn[t] = make_uint2(expert, k);
+    };
+    if (pieces) put((uint32_t)e, from, 0);
+    s_from[threadIdx.x] = from;
+    s_pieces[threadIdx.x] = pieces;
+    if (!__syncthreads_or(pieces > 1)) return;
+    for (int l = 0; l < per; ++l)
+        for (uint32_t k = 1 + threadIdx.x; k < s_pieces[l]; k += THREADS) put((uint32_t)(e0 + l), s_from[l], k);
 }
-__global__ void __launch_bounds__(THREADS) turn_count_kernel(const int32_t *__restrict__ order, uint32_t n, uint32_t C,
-                                                             uint32_t chunks, uint32_t *__restrict__ count) {
-    const uint32_t chunk = blockIdx.x * THREADS + threadIdx.x;
-    if (chunk < chunks) atomicAdd(count + bucket_of(order, chunk, C, n), 1u);
-}
+// count[b] = pieces of the parts before b; count[BUCKETS] = all
 __global__ void __launch_bounds__(1024) turn_scan_kernel(uint32_t *__restrict__ count) {
     __shared__ uint32_t warp_total[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -468,13 +527,61 @@ __global__ void __launch_bounds__(1024) turn_scan_kernel(uint32_t *__restrict__ 
     for (int q = 0; q < warp; ++q) before += warp_total[q];
     const uint4 o = make_uint4(before, before + v.x, before + v.x + v.y, before + v.x + v.y + v.z);
     reinterpret_cast<uint4 *>(count)[threadIdx.x] = o;
+    if (threadIdx.x == 1023) count[BUCKETS] = before + mine;
 }
 static_assert(BUCKETS == 4 * 1024, "turn_scan_kernel takes four counts a thread");
-__global__ void __launch_bounds__(THREADS) turn_place_kernel(const int32_t *__restrict__ order, uint32_t n, uint32_t C,
-                                                             uint32_t chunks, uint32_t *__restrict__ next,
-                                                             uint32_t *__restrict__ turn) {
-    const uint32_t chunk = blockIdx.x * THREADS + threadIdx.x;
-    if (chunk < chunks) turn[atomicAdd(next + bucket_of(order, chunk, C, n), 1u)] = chunk;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(THREADS, 4) piece_kernel(const T *__restrict__ G, uint32_t ldg,
+                                                        const float *__restrict__ w,
+                                                        const int32_t *__restrict__ offsets,
+                                                        const int32_t *__restrict__ order, uint32_t n, int K, int E,
+                                                        int D, int log_l, uint32_t C,
+                                                        const uint32_t *__restrict__ count, uint32_t most,
+                                                        const uint2 *__restrict__ turn, float *__restrict__ dF,
+                                                        float *__restrict__ partial) {
+    const int lane = threadIdx.x & 31, in_row = lane & ((1 << log_l) - 1);
+    const uint32_t t = (uint32_t)(((long long)blockIdx.x * THREADS + threadIdx.x) >> 5);
+    if (t >= min(__ldg(count + BUCKETS), most)) return;
+    const uint2 piece = __ldg(turn + t);
+    if (piece.x >= (uint32_t)E) return;
+    const uint32_t from = min((uint32_t)__ldg(offsets + piece.x), n), end = min((uint32_t)__ldg(offsets + piece.x + 1), n);
+    const uint32_t a = from + piece.y * C, b = min(a + C, end);
+    const bool whole = end - from <= C;
+    for (int slab = blockIdx.y * 32 * VEC; slab < D; slab += gridDim.y * 32 * VEC) {
+        const int c = slab + in_row * VEC;
+        float acc[VEC + 1];
+        sum_run<T, VEC>(G, ldg, w, order, n, (uint32_t)K, a, b, c, c < D, log_l, acc);
+        if (lane >> log_l == 0 && c < D)
+            store_sums<VEC>(whole ? dF + (long long)piece.x * D + c : partial + piece_row(from, piece.y, C) * D + c, acc);
+    }
+}
+
+// the partial rows of every expert of several pieces, by a warp, or by the
+// block where they are many; `per` experts a block
+__global__ void __launch_bounds__(THREADS) piece_join_kernel(const int32_t *__restrict__ offsets, uint32_t n, int E,
+                                                             int per, int D, uint32_t C,
+                                                             const float *__restrict__ partial,
+                                                             float *__restrict__ dF) {
+    __shared__ uint32_t s_from[THREADS], s_pieces[THREADS];
+    __shared__ float part[WARPS][33];
+    const int warp = threadIdx.x >> 5;
+    const long long e0 = (long long)blockIdx.x * per, e = e0 + threadIdx.x;
+    // a thread an expert first: most have no partial rows
+    uint32_t from = 0, pieces = 0;
+    if (threadIdx.x < per && e < E) {
+        from = min((uint32_t)__ldg(offsets + e), n);
+        pieces = (min((uint32_t)__ldg(offsets + e + 1), n) - from + C - 1) / C;
+    }
+    s_from[threadIdx.x] = from;
+    s_pieces[threadIdx.x] = pieces;
+    if (!__syncthreads_or(pieces > 1)) return;
+    auto rows_of = [&](uint32_t f) { return [=](uint32_t k) { return partial + piece_row(f, k, C) * D; }; };
+    for (int l = warp; l < per; l += WARPS)
+        if (s_pieces[l] > 1 && s_pieces[l] <= LONG)
+            sum_rows_warp(rows_of(s_from[l]), 0u, s_pieces[l] - 1, D, dF + (e0 + l) * D);
+    for (int l = 0; l < per; ++l)
+        if (s_pieces[l] > LONG) sum_rows_block(rows_of(s_from[l]), 0u, s_pieces[l] - 1, D, dF + (e0 + l) * D, part);
 }
 
 int ceil_log2(int v) {
@@ -598,61 +705,81 @@ cudaError_t spread_typed(RowsIn x, const int32_t *at, long long n_at, const floa
     return BY_PIECE(T, b, spread, x, at, n_at, w, rows, n, K, D, to, dots, st);
 }
 
-// Positions per chunk: about an expert's average share, so that few experts
-// are cut (a cut costs two partial rows) and few share a warp, between 128
-// (four steps of a warp) and 4096 (an expert with 2^25 pairs then leaves
-// 8192 partial rows).
-uint32_t chunk_of(long long n, int E) {
-    long long c = 128;
-    while (c < 4096 && c < n / E) c <<= 1;
+// Near rows, positions per chunk: about an expert's average share, so that
+// few experts are cut (a cut costs two partial rows) and few share a warp,
+// between 128 (four steps of a warp) and 4096 (an expert with 2^25 pairs then
+// leaves 8192 partial rows).  Far rows, positions per piece: twice that share
+// and more, so that most experts are whole.  Either way no more than leaves a
+// chunk for each of the 32 warps of a multiprocessor: 65,536 x 8 pairs of nine
+// experts in 128 chunks of 4096 took 139 us, in 4096 of 128 a tenth.
+uint32_t chunk_of(long long n, int E, bool far) {
+    long long c = far ? 512 : 128;
+    while (c < 4096 && c < n / E * (far ? 2 : 1) && c * 2 <= n / (148 * 32)) c <<= 1;
     return (uint32_t)c;
 }
 
 // dout beyond half of the L2
 constexpr size_t FAR_BYTES = 64u << 20;
+bool is_far(long long n_rows, int D, size_t element) { return (size_t)n_rows * D * element > FAR_BYTES; }
 
 size_t up(size_t v) { return (v + 255) & ~size_t(255); }
 
-// workspace: partial rows, experts cut, then counts and turns of the chunks
+// workspace: partial rows, then the experts that chunks cut, or the counts
+// and the turns of the pieces
 struct Space {
+    uint32_t C, chunks, most;  // most: pieces at most
     float *partial;
     int32_t *cut_expert;
-    uint32_t *count, *turn;
+    uint32_t *count;
+    uint2 *turn;
     size_t bytes;
-    Space(void *ws, uint32_t chunks, int D) {
+    Space(void *ws, long long n, int E, int D, bool far) {
+        C = chunk_of(n, E, far);
+        chunks = (uint32_t)((n + C - 1) / C);
+        most = chunks + (uint32_t)min((long long)E, n);
         char *p = static_cast<char *>(ws);
         partial = reinterpret_cast<float *>(p);
-        size_t at = up(sizeof(float) * 2 * (size_t)chunks * D);
+        size_t at = up(sizeof(float) * 2 * ((size_t)chunks + 1) * D);
         cut_expert = reinterpret_cast<int32_t *>(p + at);
-        at += up(sizeof(int32_t) * (size_t)chunks);
         count = reinterpret_cast<uint32_t *>(p + at);
-        at += sizeof(uint32_t) * BUCKETS;
-        turn = reinterpret_cast<uint32_t *>(p + at);
-        bytes = at + up(sizeof(uint32_t) * (size_t)chunks);
+        if (!far) {
+            bytes = at + up(sizeof(int32_t) * (size_t)chunks);
+            return;
+        }
+        at += up(sizeof(uint32_t) * (BUCKETS + 1));
+        turn = reinterpret_cast<uint2 *>(p + at);
+        bytes = at + up(sizeof(uint2) * (size_t)most);
     }
 };
 
 template <typename T, int VEC>
 cudaError_t segments(RowsIn g, const float *w, const int32_t *offsets, const int32_t *order, long long n, int K,
                      int E, int D, float *dF, void *ws, cudaStream_t st) {
-    const uint32_t C = chunk_of(n, E), chunks = (uint32_t)((n + C - 1) / C);
-    const Space s(ws, chunks, D);
-    const bool far = (size_t)(n / K) * D * sizeof(T) > FAR_BYTES;
-    if (far) {
-        const cudaError_t e = cudaMemsetAsync(s.count, 0, sizeof(uint32_t) * BUCKETS, st);
-        if (e != cudaSuccess) return e;
-        const unsigned blocks = (chunks + THREADS - 1) / THREADS;
-        turn_count_kernel<<<blocks, THREADS, 0, st>>>(order, (uint32_t)n, C, chunks, s.count);
-        turn_scan_kernel<<<1, 1024, 0, st>>>(s.count);
-        turn_place_kernel<<<blocks, THREADS, 0, st>>>(order, (uint32_t)n, C, chunks, s.count, s.turn);
+    const bool far = is_far(n / K, D, sizeof(T));
+    const Space s(ws, n, E, D, far);
+    const T *G = static_cast<const T *>(g.p);
+    const unsigned slabs = (unsigned)min((D + 32 * VEC - 1) / (32 * VEC), 65535);
+    const uint32_t m = (uint32_t)n;
+    if (!far) {
+        const dim3 grid((s.chunks + WARPS - 1) / WARPS, slabs);
+        chunk_kernel<T, VEC><<<grid, THREADS, 0, st>>>(G, row_bytes<T>(g.ld), w, offsets, order, m, K, E, D,
+                                                       group_log(D, VEC), s.C, s.chunks, dF, s.partial, s.cut_expert);
+        if (s.chunks > 1)
+            join_kernel<<<(s.chunks + WARPS - 1) / WARPS, THREADS, 0, st>>>(offsets, s.cut_expert, m, E, D, s.C,
+                                                                            s.chunks, s.partial, dF);
+        return cudaGetLastError();
     }
-    const dim3 grid((chunks + WARPS - 1) / WARPS, (unsigned)min((D + 32 * VEC - 1) / (32 * VEC), 65535));
-    segment_kernel<T, VEC><<<grid, THREADS, 0, st>>>(static_cast<const T *>(g.p), row_bytes<T>(g.ld), w, offsets,
-                                                     order, (uint32_t)n, K, E, D, group_log(D, VEC), C, chunks,
-                                                     far ? s.turn : nullptr, dF, s.partial, s.cut_expert);
-    if (chunks > 1)
-        join_kernel<<<(chunks + WARPS - 1) / WARPS, THREADS, 0, st>>>(offsets, s.cut_expert, (uint32_t)n, E, D, C,
-                                                                      chunks, s.partial, dF);
+    const cudaError_t e = cudaMemsetAsync(s.count, 0, sizeof(uint32_t) * (BUCKETS + 1), st);
+    if (e != cudaSuccess) return e;
+    const int per = E <= 1024 ? 1 : E <= 16384 ? 16 : THREADS;
+    const unsigned experts = (unsigned)(((long long)E + per - 1) / per);
+    turn_kernel<false><<<experts, THREADS, 0, st>>>(offsets, order, m, E, per, s.C, s.count, s.most, s.turn);
+    turn_scan_kernel<<<1, 1024, 0, st>>>(s.count);
+    turn_kernel<true><<<experts, THREADS, 0, st>>>(offsets, order, m, E, per, s.C, s.count, s.most, s.turn);
+    const dim3 grid((s.most + WARPS - 1) / WARPS, slabs);
+    piece_kernel<T, VEC><<<grid, THREADS, 0, st>>>(G, row_bytes<T>(g.ld), w, offsets, order, m, K, E, D,
+                                                   group_log(D, VEC), s.C, s.count, s.most, s.turn, dF, s.partial);
+    piece_join_kernel<<<experts, THREADS, 0, st>>>(offsets, m, E, per, D, s.C, s.partial, dF);
     return cudaGetLastError();
 }
 
@@ -679,9 +806,9 @@ cudaError_t launch_spread(int dtype, RowsIn x, const int32_t *at, long long n_at
 }
 
 size_t segment_workspace_bytes(long long n_rows, int K, int E, int D) {
+    // of any element type: whether rows are far depends on it
     const long long n = n_rows * K;
-    const uint32_t C = chunk_of(n, E);
-    return Space(nullptr, (uint32_t)((n + C - 1) / C), D).bytes;
+    return max(Space(nullptr, n, E, D, false).bytes, is_far(n_rows, D, 4) ? Space(nullptr, n, E, D, true).bytes : 0);
 }
 
 cudaError_t launch_segment_sums(int dtype, RowsIn dout, const float *w, const int32_t *offsets, const int32_t *order,
