@@ -642,10 +642,57 @@ cudaError_t route_by_runs(const int32_t *ids, long long n, int E, const Plan &p,
     return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// few pairs: one launch
+// ---------------------------------------------------------------------------
+// A pair's place is the number of words (key, pair) below its own: every
+// thread of a block compares its pair with all of them, four to a load.  Each
+// block does the same for its share of the offsets, found by bisection.
+constexpr int FEW = 1024;
+constexpr int FEW_OFFSETS = 8192;  // a block
+__global__ void __launch_bounds__(FEW) few_kernel(const int32_t *__restrict__ ids, int n, int E,
+                                                  int32_t *__restrict__ offsets, int32_t *__restrict__ order,
+                                                  int32_t *__restrict__ place) {
+    __shared__ __align__(16) uint32_t word[FEW];
+    __shared__ uint32_t sorted[FEW];
+    const int j = threadIdx.x;
+    const uint32_t key = j < n ? key_of(__ldg(ids + j), E) : 0, mine = j < n ? key << 10 | (uint32_t)j : 0xffffffffu;
+    word[j] = mine;
+    __syncthreads();
+    int rank = 0;
+    const uint4 *four = reinterpret_cast<const uint4 *>(word);
+    for (int i = 0; i < (n + 3) / 4; ++i) {
+        const uint4 v = four[i];
+        rank += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
+    }
+    if (j < n) {
+        sorted[rank] = key;
+        if (blockIdx.x == 0) {
+            const bool empty = key == (uint32_t)E;
+            order[rank] = empty ? -1 : j;
+            place[j] = empty ? -1 : rank;
+        }
+    }
+    __syncthreads();
+    const int last = min(E, (blockIdx.x + 1) * FEW_OFFSETS - 1);
+    for (int e = blockIdx.x * FEW_OFFSETS + j; e <= last; e += blockDim.x) {
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (sorted[mid] < (uint32_t)e) lo = mid + 1;
+            else hi = mid;
+        }
+        offsets[e] = lo;
+    }
+}
+// the word has 22 bits for the key
+bool is_few(long long n, int E) { return n <= FEW && E < 1 << 22; }
+
 }  // namespace
 
 size_t route_workspace_bytes(long long n_rows, int K, int E) {
     const long long n = n_rows * K;
+    if (is_few(n, E)) return up(1);  // none needed: every size has some
     const Plan p = make_plan(n, E);
     if (p.by_runs) return RunSpace(nullptr, n, p).bytes;
     const size_t table = up(sizeof(uint32_t) << p.bits) + up((sizeof(uint32_t) << p.bits) * p.blocks);
@@ -658,6 +705,11 @@ cudaError_t launch_route(const int32_t *ids, long long n_rows, int K, int E, int
                          int32_t *place, void *ws, cudaStream_t st) {
     const long long n = n_rows * K;
     if (n == 0) return cudaMemsetAsync(offsets, 0, sizeof(int32_t) * ((size_t)E + 1), st);
+    if (is_few(n, E)) {
+        const int threads = n <= 32 ? 128 : ((int)n + 31) / 32 * 32;
+        few_kernel<<<E / FEW_OFFSETS + 1, threads, 0, st>>>(ids, (int)n, E, offsets, order, place);
+        return cudaGetLastError();
+    }
     const Plan p = make_plan(n, E);
     if (p.by_runs) return route_by_runs(ids, n, E, p, offsets, order, place, ws, st);
     const int D = 1 << p.bits;

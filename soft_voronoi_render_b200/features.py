@@ -54,22 +54,27 @@ def _dense(name: str, x, dtype, shape, device):
         _refuse(f"{name} must be dense and on {device}")
 
 
-class _On:
-    """The tensors' device made current for one call, where it is not."""
+# The current stream's handle by device index.  torch.cuda.current_stream()
+# builds a Stream object first, 3 us of a call's 10.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("guard",)
 
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _run(device, call, *args):
+    """call(*args, stream) on the current stream of the tensors' device, made
+    current for the call where it is not; raises on a non-zero status."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, _raw_stream(index))
+    if status:
+        raise SadError(status, _lib.sad_feature_error())
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _at(x):
+    return None if x is None else x.data_ptr()
 
 
 class Route:
@@ -96,11 +101,14 @@ class Route:
         self.device = self.offsets.device
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=device)
 
+    @property
+    def _outputs(self):
+        return (self.offsets.data_ptr(), self.order.data_ptr(), self.place.data_ptr(), self.workspace.data_ptr(),
+                self.workspace.numel())
+
     def build(self, ids) -> "Route":
         _dense("ids", ids, torch.int32, (self.T, self.K), self.device)
-        with _On(self.device) as st:
-            _lib.sad_route(ids, self.T, self.K, self.E, self.offsets, self.order, self.place, self.workspace,
-                           self.workspace.numel(), st)
+        _run(self.device, _lib.load().sad_route, ids.data_ptr(), self.T, self.K, self.E, *self._outputs)
         return self
 
     def _weights(self, weights):
@@ -121,11 +129,13 @@ class Route:
         if x.shape[0] != self.T:
             _refuse(f"x has {x.shape[0]} rows, the route {self.T}")
         self._weights(weights)
+        ldo = D
         if out is None:
-            out = torch.empty((self.T * self.K, D), dtype=x.dtype, device=x.device)
-        ldo = _rows("out", out, (self.T * self.K, D), x)
-        with _On(self.device) as st:
-            _lib.sad_dispatch(_TYPES[x.dtype], x, ldx, weights, self.place, self.T, self.K, D, out, ldo, st)
+            out = x.new_empty((self.T * self.K, D))
+        else:
+            ldo = _rows("out", out, (self.T * self.K, D), x)
+        _run(self.device, _lib.load().sad_dispatch, _TYPES[x.dtype], x.data_ptr(), ldx, _at(weights),
+             self.place.data_ptr(), self.T, self.K, D, out.data_ptr(), ldo)
         return out
 
     def dispatch_backward(self, dxs, x=None, weights=None, dx=None):
@@ -140,13 +150,14 @@ class Route:
         ldx, dw = 0, None
         if x is not None:
             ldx = _rows("x", x, (self.T, D), dxs)
-            dw = torch.empty((self.T, self.K), dtype=torch.float32, device=x.device)
+            dw = x.new_empty((self.T, self.K), dtype=torch.float32)
+        lddx = D
         if dx is None:
-            dx = torch.empty((self.T, D), dtype=dxs.dtype, device=dxs.device)
-        lddx = _rows("dx", dx, (self.T, D), dxs)
-        with _On(self.device) as st:
-            _lib.sad_dispatch_backward(_TYPES[dxs.dtype], dxs, ld, x, ldx, weights, self.place, self.T, self.K, D, dx,
-                                       lddx, dw, st)
+            dx = dxs.new_empty((self.T, D))
+        else:
+            lddx = _rows("dx", dx, (self.T, D), dxs)
+        _run(self.device, _lib.load().sad_dispatch_backward, _TYPES[dxs.dtype], dxs.data_ptr(), ld, _at(x), ldx,
+             _at(weights), self.place.data_ptr(), self.T, self.K, D, dx.data_ptr(), lddx, _at(dw))
         return dx, dw
 
     def combine(self, y, weights=None, out=None):
@@ -158,11 +169,13 @@ class Route:
         if y.shape[0] != self.T * self.K:
             _refuse(f"y has {y.shape[0]} rows, the route {self.T * self.K} pairs")
         self._weights(weights)
+        ldo = D
         if out is None:
-            out = torch.empty((self.T, D), dtype=y.dtype, device=y.device)
-        ldo = _rows("out", out, (self.T, D), y)
-        with _On(self.device) as st:
-            _lib.sad_combine(_TYPES[y.dtype], y, ldy, weights, self.place, self.T, self.K, D, out, ldo, st)
+            out = y.new_empty((self.T, D))
+        else:
+            ldo = _rows("out", out, (self.T, D), y)
+        _run(self.device, _lib.load().sad_combine, _TYPES[y.dtype], y.data_ptr(), ldy, _at(weights),
+             self.place.data_ptr(), self.T, self.K, D, out.data_ptr(), ldo)
         return out
 
     def combine_backward(self, dout, y=None, weights=None, dy=None):
@@ -178,13 +191,14 @@ class Route:
         ldy, dw = 0, None
         if y is not None:
             ldy = _rows("y", y, (self.T * self.K, D), dout)
-            dw = torch.empty((self.T, self.K), dtype=torch.float32, device=y.device)
+            dw = y.new_empty((self.T, self.K), dtype=torch.float32)
+        lddy = D
         if dy is None:
-            dy = torch.empty((self.T * self.K, D), dtype=dout.dtype, device=dout.device)
-        lddy = _rows("dy", dy, (self.T * self.K, D), dout)
-        with _On(self.device) as st:
-            _lib.sad_combine_backward(_TYPES[dout.dtype], dout, ld, y, ldy, weights, self.place, self.T, self.K, D,
-                                      dy, lddy, dw, st)
+            dy = dout.new_empty((self.T * self.K, D))
+        else:
+            lddy = _rows("dy", dy, (self.T * self.K, D), dout)
+        _run(self.device, _lib.load().sad_combine_backward, _TYPES[dout.dtype], dout.data_ptr(), ld, _at(y), ldy,
+             _at(weights), self.place.data_ptr(), self.T, self.K, D, dy.data_ptr(), lddy, _at(dw))
         return dy, dw
 
 
@@ -202,11 +216,13 @@ def blend(F, ids, weights, out=None):
     ldf = _rows("F", F)
     T, K = _lists(ids, weights, F.device)
     E, D = F.shape
+    ldo = D
     if out is None:
-        out = torch.empty((T, D), dtype=F.dtype, device=F.device)
-    ldo = _rows("out", out, (T, D), F)
-    with _On(F.device) as st:
-        _lib.sad_blend(_TYPES[F.dtype], F, ldf, E, ids, weights, T, K, D, out, ldo, st)
+        out = F.new_empty((T, D))
+    else:
+        ldo = _rows("out", out, (T, D), F)
+    _run(F.device, _lib.load().sad_blend, _TYPES[F.dtype], F.data_ptr(), ldf, E, ids.data_ptr(), weights.data_ptr(),
+         T, K, D, out.data_ptr(), ldo)
     return out
 
 
@@ -220,7 +236,7 @@ def blend_backward(dout, F, ids, weights, route=None, dF=None):
     if tuple(dout.shape) != (T, D):
         _refuse(f"dout has shape {tuple(dout.shape)}, expected {(T, D)}")
     dev = F.device
-    dw = torch.empty((T, K), dtype=torch.float32, device=dev)
+    dw = weights.new_empty((T, K))
     offsets = order = ws = None
     nbytes = 0
     if route is not None:
@@ -228,15 +244,15 @@ def blend_backward(dout, F, ids, weights, route=None, dF=None):
             _refuse("the route was made for other sizes or another device")
         offsets, order = route.offsets, route.order
         if dF is None:
-            dF = torch.empty((E, D), dtype=torch.float32, device=dev)
-        _dense("dF", dF, torch.float32, (E, D), dev)
+            dF = weights.new_empty((E, D))
+        else:
+            _dense("dF", dF, torch.float32, (E, D), dev)
         nbytes = _lib.sad_blend_workspace_bytes(T, K, E, D)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        ws = weights.new_empty(-(-nbytes // 4))
     elif dF is not None:
         _refuse("dF needs a route")
-    with _On(dev) as st:
-        _lib.sad_blend_backward(_TYPES[F.dtype], dout, ld, F, ldf, E, ids, weights, offsets, order, T, K, D, dF, dw,
-                                ws, nbytes, st)
+    _run(dev, _lib.load().sad_blend_backward, _TYPES[F.dtype], dout.data_ptr(), ld, F.data_ptr(), ldf, E,
+         ids.data_ptr(), weights.data_ptr(), _at(offsets), _at(order), T, K, D, _at(dF), dw.data_ptr(), _at(ws), nbytes)
     return dF, dw
 
 
@@ -249,13 +265,14 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, out=None):
     for name, v in (("gamma", gamma), ("beta", beta)):
         if v is not None:
             _dense(name, v, torch.float32, (D,), dev)
+    ldy = D
     if out is None:
-        out = torch.empty((T, D), dtype=x.dtype, device=dev)
-    ldy = _rows("out", out, (T, D), x)
-    stats = torch.empty((2, T), dtype=torch.float32, device=dev)
-    mean, rstd = stats[0], stats[1]
-    with _On(dev) as st:
-        _lib.sad_layer_norm(_TYPES[x.dtype], x, ldx, gamma, beta, eps, T, D, out, ldy, mean, rstd, st)
+        out = x.new_empty((T, D))
+    else:
+        ldy = _rows("out", out, (T, D), x)
+    mean, rstd = x.new_empty(T, dtype=torch.float32), x.new_empty(T, dtype=torch.float32)
+    _run(dev, _lib.load().sad_layer_norm, _TYPES[x.dtype], x.data_ptr(), ldx, _at(gamma), _at(beta), eps, T, D,
+         out.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr())
     return out, mean, rstd
 
 
@@ -271,19 +288,19 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, want_affine: bool = True, dx=N
         _dense("gamma", gamma, torch.float32, (D,), dev)
     _dense("mean", mean, torch.float32, (T,), dev)
     _dense("rstd", rstd, torch.float32, (T,), dev)
+    lddx = D
     if dx is None:
-        dx = torch.empty((T, D), dtype=x.dtype, device=dev)
-    lddx = _rows("dx", dx, (T, D), x)
+        dx = x.new_empty((T, D))
+    else:
+        lddx = _rows("dx", dx, (T, D), x)
     dgamma = dbeta = ws = None
     nbytes = 0
     if want_affine:
-        grads = torch.empty((2, D), dtype=torch.float32, device=dev)
-        dgamma, dbeta = grads[0], grads[1]
+        dgamma, dbeta = mean.new_empty(D), mean.new_empty(D)
         nbytes = _lib.sad_layer_norm_workspace_bytes(T, D)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with _On(dev) as st:
-        _lib.sad_layer_norm_backward(_TYPES[x.dtype], dy, ld, x, ldx, gamma, mean, rstd, T, D, dx, lddx, dgamma,
-                                     dbeta, ws, nbytes, st)
+        ws = mean.new_empty(-(-nbytes // 4))
+    _run(dev, _lib.load().sad_layer_norm_backward, _TYPES[x.dtype], dy.data_ptr(), ld, x.data_ptr(), ldx, _at(gamma),
+         mean.data_ptr(), rstd.data_ptr(), T, D, dx.data_ptr(), lddx, _at(dgamma), _at(dbeta), _at(ws), nbytes)
     return dx, dgamma, dbeta
 
 
@@ -303,15 +320,14 @@ def distill(logits, teacher_ids, teacher_logits, temperature: float = 1.0, row_w
     _dense("teacher_logits", teacher_logits, torch.float32, (T, M), dev)
     if row_weight is not None:
         _dense("row_weight", row_weight, torch.float32, (T,), dev)
-    lddz = 0
-    if dlogits is not None or want_grad:
-        if dlogits is None:
-            dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev)
+    lddz = V
+    if dlogits is not None:
         lddz = _rows("dlogits", dlogits, (T, V), logits)
-    loss = torch.empty(T, dtype=torch.float32, device=dev)
-    with _On(dev) as st:
-        _lib.sad_distill(_TYPES[logits.dtype], logits, ld, teacher_ids, teacher_logits, row_weight, T, V, M,
-                         float(temperature), loss, dlogits, lddz, st)
+    elif want_grad:
+        dlogits = logits.new_empty((T, V))
+    loss = teacher_logits.new_empty(T)
+    _run(dev, _lib.load().sad_distill, _TYPES[logits.dtype], logits.data_ptr(), ld, teacher_ids.data_ptr(),
+         teacher_logits.data_ptr(), _at(row_weight), T, V, M, float(temperature), loss.data_ptr(), _at(dlogits), lddz)
     return loss, dlogits
 
 
