@@ -52,6 +52,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
+// 1 / x, within 1 ulp
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ float minus_infinity() { return __int_as_float(0xff800000); }
 
 // A maximum to subtract: 0 for a row, or part of one, of nothing but -infinity
@@ -72,15 +79,13 @@ struct Teacher {
     int32_t *id;  // -1: does not count
     float *q;     // first the logit (base 2), then the probability
     float *zid;   // the student's logit of the class (base 2)
-    float max, sum;
-    bool any;
+    float max, sum;  // the largest logit, -infinity where no entry counts
 };
 
 template <typename T>
 __device__ __forceinline__ void teacher_load(Teacher &t, const int32_t *__restrict__ tid, const float *__restrict__ tl,
                                              const T *row, int V, int M, float k, bool in, int lane, int L) {
     float big = minus_infinity();
-    bool any = false;
     for (int m = lane; m < M; m += L) {
         int32_t id = in ? __ldg(tid + m) : -1;
         float l = minus_infinity(), z = 0.0f;
@@ -89,21 +94,16 @@ __device__ __forceinline__ void teacher_load(Teacher &t, const int32_t *__restri
             z = to_f32<T>(row[id]) * k;
         }
         if (l == minus_infinity()) id = -1;  // a NaN logit of a valid class counts, and shows
-        any = any || id >= 0;
         big = max_nan(big, l);
         t.id[m] = id;
         t.q[m] = l;
         t.zid[m] = z;
     }
     t.max = big;
-    t.any = any;
 }
 
 __device__ __forceinline__ void teacher_softmax(Teacher &t, int M, int lane, int L) {
     t.max = lanes_max(t.max, L);
-    int any = t.any;
-    for (int o = L >> 1; o; o >>= 1) any |= __shfl_xor_sync(0xffffffffu, any, o);
-    t.any = any;
     float s = 0.0f;
     const float m0 = finite_max(t.max);
     for (int m = lane; m < M; m += L) s += exp2_fast(t.q[m] - m0);
@@ -113,7 +113,7 @@ __device__ __forceinline__ void teacher_softmax(Teacher &t, int M, int lane, int
 // the row's divergence (before rw tau^2), given the student's maximum and sum;
 // leaves q in shared memory
 __device__ __forceinline__ float teacher_loss(Teacher &t, int M, int lane, int L, float big, float sum) {
-    const float is = 1.0f / t.sum, lt = log2f(t.sum), ls = log2f(sum);
+    const float is = reciprocal(t.sum), more = log2f(sum * is);
     const float m0 = finite_max(t.max);
     float part = 0.0f;
     for (int m = lane; m < M; m += L) {
@@ -121,8 +121,8 @@ __device__ __forceinline__ float teacher_loss(Teacher &t, int M, int lane, int L
         if (t.id[m] >= 0) {
             const float l = t.q[m] - m0;
             q = exp2_fast(l) * is;
-            // ln q - ln p with both maxima taken out first
-            if (q != 0.0f) part = fmaf(q, (l - lt) - ((t.zid[m] - big) - ls), part);
+            // log q - log p with both maxima taken out first
+            if (q != 0.0f) part = fmaf(q, (l - (t.zid[m] - big)) + more, part);
         }
         t.q[m] = q;
     }
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     for (int i = 0; i < NV; ++i)
         if (lane + i * L < pieces) big = piece_max(p[i], big);
     big = lanes_max(big, L) * k;
-    const bool live = te.any && weight != 0.0f && big != minus_infinity();
+    const bool live = te.max != minus_infinity() && weight != 0.0f && big != minus_infinity();
     if (!live) {  // the row may hold anything: take 0 for it
 #pragma unroll
         for (int i = 0; i < NV; ++i) p[i].clear();
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     const float part = teacher_loss(te, M, lane, L, big, sum);
     if (lane == 0 && in) loss[t] = live ? weight * tau * tau * part : 0.0f;
     if (!GRAD) return;
-    const float scale = weight * tau, is = 1.0f / sum, f = live ? scale * is : 0.0f;
+    const float scale = weight * tau, is = reciprocal(sum), f = live ? scale * is : 0.0f;
     T *out = dz + t * lddz;
     const bool whole = !EDGES || same_boundaries(out, row);
 #pragma unroll
@@ -330,11 +330,11 @@ __global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
     const int first = min(rank * each, cut.pieces), last = min(first + each, cut.pieces);
     const T *body = row + cut.head;
 
-    Teacher te{s_id, s_q, s_zid, 0.0f, 0.0f, false};
+    Teacher te{s_id, s_q, s_zid, 0.0f, 0.0f};
     if (warp == 0) {
         teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, k, true, lane, 32);
         teacher_softmax(te, M, lane, 32);
-        if (lane == 0) t_any = te.any ? 1.0f : 0.0f;
+        if (lane == 0) t_any = te.max != minus_infinity() ? 1.0f : 0.0f;
     }
 
     // each thread's running maximum (as loaded) and sum of exponentials about
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
         if (lane == 0 && rank == 0) loss[t] = live ? weight * tau * tau * part : 0.0f;
     }
     if (!GRAD) return;
-    const float scale = weight * tau, is = 1.0f / sum, f = scale * is;
+    const float scale = weight * tau, is = reciprocal(sum), f = scale * is;
     T *out = dz + t * lddz, *out_body = out + cut.head;
     const bool whole = same_boundaries(out, row);
     if (edge < V) out[edge] = from_f32<T>(live ? exp2_fast(fmaf(edge_z, k, -big)) * f : 0.0f);
@@ -499,17 +499,17 @@ template <typename T, int VEC, bool EDGES> cudaError_t group_shape(RowsIn z, Row
 template <typename T> cudaError_t long_launch(RowsIn z, RowsOut dz, const Args &a, cudaStream_t st) {
     constexpr int VEC = 16 / sizeof(T);
     const int pieces = (a.V + VEC - 1) / VEC;
-    constexpr int FIT = 100 * 1024 / 16, MOST = 200 * 1024 / 16;  // pieces in shared memory: two blocks, or one
+    constexpr int FIT = 100 * 1024 / 16, CACHED = 48 * 1024 / 16;
     // blocks of a cluster: what shared memory asks for, and more while there
     // are multiprocessors without a row and 8 KB for each block
     int ranks = 1;
     while (ranks < 8 && (pieces > ranks * FIT || (a.n * ranks * 2 <= SMS && pieces >= ranks * 2 * LONG_THREADS)))
         ranks *= 2;
     const int each = (pieces + ranks - 1) / ranks;
-    const bool cached = each <= MOST;
+    const bool cached = each <= CACHED;
     // about eight pieces a thread: with more threads a block of short rows
     // waits for its reductions most of the time
-    const int threads = each <= 1024 ? 128 : each <= 2048 ? 256 : LONG_THREADS;
+    const int threads = each <= 1024 ? 128 : 256;
     const size_t shared = dz.p && cached ? (size_t)each * 16 : 0;
     auto kernel = !dz.p ? distill_long_kernel<T, false, true>
                         : cached ? distill_long_kernel<T, true, true> : distill_long_kernel<T, true, false>;

@@ -233,14 +233,15 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
             Pack<T, VEC> p[K_MAX];
             if (DOT) {
 #pragma unroll
-                for (int k = 0; k < K_MAX; ++k) {
-                    p[k].clear();
+                for (int k = 0; k < K_MAX; ++k)
                     if (id[k] < n_at) p[k] = load_pack<T, VEC>(at_row(R, id[k], ldr, c));
-                }
             }
             const Pack<T, VEC> x = load_pack<T, VEC>(at_row(X, (uint32_t)me.t, ldx, c));
 #pragma unroll
             for (int k = 0; k < K_MAX; ++k) {
+                // a branch here only with the products: 172 us against 224 for the
+                // 16384 x 8 x 2048 bf16 backward, but 105 against 100 without
+                if (DOT && id[k] >= n_at) continue;
                 float f[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
                 }
                 Pack<T, VEC> o;
                 o.set(f);
-                if (id[k] < n_at) store_pack<T, VEC>(const_cast<T *>(at_row(S, id[k], lds, c)), o);
+                if (DOT || id[k] < n_at) store_pack<T, VEC>(const_cast<T *>(at_row(S, id[k], lds, c)), o);
             }
         }
     }
