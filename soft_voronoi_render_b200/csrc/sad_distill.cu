@@ -306,10 +306,12 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
 // ---------------------------------------------------------------------------
 // long rows: a block or a cluster each
 // ---------------------------------------------------------------------------
-constexpr int LONG_THREADS = 512;
+constexpr int LONG_THREADS = 256;
 
+// The last warp has the teacher's side: its chain of loads (ids, then the
+// student's logits of them) and its sums over repeated ids run beside the row.
 template <typename T, bool GRAD, bool CACHE>
-__global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
+__global__ void __launch_bounds__(LONG_THREADS + 32, 4) distill_long_kernel(
     const T *z, long long ldz, const int32_t *__restrict__ tid, const float *__restrict__ tl,
     const float *__restrict__ rw, int V, int M, float tau, int each, float *__restrict__ loss, T *dz,
     long long lddz) {
@@ -321,17 +323,19 @@ __global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
     __shared__ float block_max, block_sum, t_any;
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, B = blockDim.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int B = blockDim.x - 32, warps = B >> 5;  // of the row
+    const bool has_teacher = warp == warps;
     const long long t = blockIdx.x / ranks;
     const T *row = z + t * ldz;
     const float k = LOG2E / tau;
     const float weight = rw ? __ldg(rw + t) : 1.0f;
     const Cut<T, VEC> cut(row, V, true);
-    const int first = min(rank * each, cut.pieces), last = min(first + each, cut.pieces);
+    const int first = min(rank * each, cut.pieces), last = has_teacher ? first : min(first + each, cut.pieces);
     const T *body = row + cut.head;
 
     Teacher te{s_id, s_q, s_zid, 0.0f, 0.0f};
-    if (warp == 0) {
+    if (has_teacher) {
         teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, k, true, lane, 32);
         teacher_softmax(te, M, lane, 32);
         if (lane == 0) t_any = te.max != minus_infinity() ? 1.0f : 0.0f;
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
 
     // each thread's running maximum (as loaded) and sum of exponentials about
     // it; one thread of the first block takes an edge each
-    const int edge = rank ? V : cut.edge(threadIdx.x, V);
+    const int edge = rank || has_teacher ? V : cut.edge(threadIdx.x, V);
     float big = minus_infinity(), sum = 0.0f;
     if (edge < V) {
         big = to_f32<T>(row[edge]);
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
     {
         const float m = lanes_max(big, 32);
         const float s = lanes_sum(big == minus_infinity() ? 0.0f : sum * exp2_fast((big - finite_max(m)) * k), 32);
-        if (lane == 0) s_max[warp] = m, s_sum[warp] = s;
+        if (lane == 0 && !has_teacher) s_max[warp] = m, s_sum[warp] = s;
     }
     __syncthreads();
     {
@@ -400,12 +404,16 @@ __global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
     }
     big *= k;
     const bool live = t_any != 0.0f && weight != 0.0f && big != minus_infinity();
-    if (warp == 0) {
+    const float scale = weight * tau, is = reciprocal(sum), f = scale * is;
+    if (has_teacher) {
         const float part = teacher_loss(te, M, lane, 32, big, sum);
         if (lane == 0 && rank == 0) loss[t] = live ? weight * tau * tau * part : 0.0f;
+        if (GRAD) {
+            __syncwarp();
+            for (int m = lane; m < M; m += 32) s_zid[m] = teacher_grad(te, M, m, big, is, scale);
+        }
     }
     if (!GRAD) return;
-    const float scale = weight * tau, is = reciprocal(sum), f = scale * is;
     T *out = dz + t * lddz, *out_body = out + cut.head;
     const bool whole = same_boundaries(out, row);
     if (edge < V) out[edge] = from_f32<T>(live ? exp2_fast(fmaf(edge_z, k, -big)) * f : 0.0f);
@@ -432,12 +440,12 @@ __global__ void __launch_bounds__(LONG_THREADS, 2) distill_long_kernel(
     }
     __syncthreads();
     // the teacher's classes in this block's part, from float32
+    const int end = min(first + each, cut.pieces);
     if (live)
-        for (int m = threadIdx.x; m < M; m += B) {
+        for (int m = threadIdx.x; m < M; m += blockDim.x) {
             if (s_id[m] < 0) continue;
             const int piece = cut.piece_of(s_id[m], V);
-            if (piece < 0 ? rank == 0 : (piece >= first && piece < last))
-                out[s_id[m]] = from_f32<T>(teacher_grad(te, M, m, big, is, scale));
+            if (piece < 0 ? rank == 0 : (piece >= first && piece < end)) out[s_id[m]] = from_f32<T>(s_zid[m]);
         }
 }
 
@@ -507,9 +515,9 @@ template <typename T> cudaError_t long_launch(RowsIn z, RowsOut dz, const Args &
         ranks *= 2;
     const int each = (pieces + ranks - 1) / ranks;
     const bool cached = each <= CACHED;
-    // about eight pieces a thread: with more threads a block of short rows
-    // waits for its reductions most of the time
-    const int threads = each <= 1024 ? 128 : 256;
+    // eight pieces a thread, two rounds of loads: with more threads a block of
+    // short rows waits for its reductions most of the time
+    const int threads = min(LONG_THREADS, max(64, (each + 255) / 256 * 32)) + 32;
     const size_t shared = dz.p && cached ? (size_t)each * 16 : 0;
     auto kernel = !dz.p ? distill_long_kernel<T, false, true>
                         : cached ? distill_long_kernel<T, true, true> : distill_long_kernel<T, true, false>;
