@@ -68,6 +68,21 @@ __device__ __forceinline__ float lanes_sum(float v, int L) {
     for (int o = L >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// two at a time
+__device__ __forceinline__ void lanes_sum(float &a, float &b, int L) {
+    for (int o = L >> 1; o; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, a, o), v = __shfl_xor_sync(0xffffffffu, b, o);
+        a += u;
+        b += v;
+    }
+}
+__device__ __forceinline__ void lanes_max(float &a, float &b, int L) {
+    for (int o = L >> 1; o; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, a, o), v = __shfl_xor_sync(0xffffffffu, b, o);
+        a = max_nan(a, u);
+        b = max_nan(b, v);
+    }
+}
 __device__ __forceinline__ float lanes_max(float v, int L) {
     for (int o = L >> 1; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
@@ -102,12 +117,12 @@ __device__ __forceinline__ void teacher_load(Teacher &t, const int32_t *__restri
     t.max = big;
 }
 
-__device__ __forceinline__ void teacher_softmax(Teacher &t, int M, int lane, int L) {
-    t.max = lanes_max(t.max, L);
+// a lane's share of the sum of exponentials about t.max
+__device__ __forceinline__ float teacher_sum(const Teacher &t, int M, int lane, int L) {
     float s = 0.0f;
     const float m0 = finite_max(t.max);
     for (int m = lane; m < M; m += L) s += exp2_fast(t.q[m] - m0);
-    t.sum = lanes_sum(s, L);
+    return s;
 }
 
 // the row's divergence (before rw tau^2), given the student's maximum and sum;
@@ -133,6 +148,7 @@ __device__ __forceinline__ float teacher_loss(Teacher &t, int M, int lane, int L
 __device__ __forceinline__ float teacher_grad(const Teacher &t, int M, int m, float big, float inv_sum, float scale) {
     const int32_t id = t.id[m];
     float q = 0.0f;
+#pragma unroll 4
     for (int j = 0; j < M; ++j)
         if (t.id[j] == id) q += t.q[j];
     return scale * (exp2_fast(t.zid[m] - big) * inv_sum - q);
@@ -257,13 +273,13 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     te.q = space + M;
     te.zid = space + 2 * M;
     teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, k, in, lane, L);
-    teacher_softmax(te, M, lane, L);
 
     float big = EDGES ? edge_z : minus_infinity();
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (lane + i * L < pieces) big = piece_max(p[i], big);
-    big = lanes_max(big, L) * k;
+    lanes_max(big, te.max, L);
+    big *= k;
     const bool live = te.max != minus_infinity() && weight != 0.0f && big != minus_infinity();
     if (!live) {  // the row may hold anything: take 0 for it
 #pragma unroll
@@ -284,7 +300,9 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     both(sums, sum, other);
     sum += other;
     const float edge_e = EDGES && edge < V ? exp2_fast(fmaf(edge_z, k, -big)) : 0.0f;
-    sum = lanes_sum(sum + edge_e, L);
+    sum += edge_e;
+    te.sum = teacher_sum(te, M, lane, L);
+    lanes_sum(sum, te.sum, L);
     const float part = teacher_loss(te, M, lane, L, big, sum);
     if (lane == 0 && in) loss[t] = live ? weight * tau * tau * part : 0.0f;
     if (!GRAD) return;
@@ -337,7 +355,8 @@ __global__ void __launch_bounds__(LONG_THREADS + 32, 4) distill_long_kernel(
     Teacher te{s_id, s_q, s_zid, 0.0f, 0.0f};
     if (has_teacher) {
         teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, k, true, lane, 32);
-        teacher_softmax(te, M, lane, 32);
+        te.max = lanes_max(te.max, 32);
+        te.sum = lanes_sum(teacher_sum(te, M, lane, 32), 32);
         if (lane == 0) t_any = te.max != minus_infinity() ? 1.0f : 0.0f;
     }
 
@@ -481,14 +500,16 @@ constexpr int GROUP_PIECES = 8;  // a lane, at most
 
 template <typename T, int VEC, bool EDGES> cudaError_t group_shape(RowsIn z, RowsOut dz, const Args &a, cudaStream_t st) {
     const int pieces = EDGES ? max(1, a.V / VEC) : (a.V + VEC - 1) / VEC;
-    // the lanes that leave the fewest idle, the fewest on a tie; enough of
-    // them for every edge, and that the groups' teachers fit 48 KB
+    // the lanes that leave the fewest idle, the most on a tie (the gradient
+    // keeps a register for every element: 65,536 x 1000 bf16 in 72 us with 32
+    // lanes, 82 with 16); enough for every edge, and that the groups' teachers
+    // fit 48 KB
     const int least = EDGES ? 2 * (VEC - 1) : 1;
     int log_l = 5, best = 1 << 30;
     for (int l = 0; l <= 5; ++l) {
         const int each = (pieces + (1 << l) - 1) >> l;
         if ((1 << l) < least || each > GROUP_PIECES || (GROUP_THREADS >> l) * a.M * 12 > 48 * 1024) continue;
-        if ((each << l) < best) {
+        if ((each << l) <= best) {
             best = each << l;
             log_l = l;
         }
@@ -508,8 +529,9 @@ template <typename T> cudaError_t long_launch(RowsIn z, RowsOut dz, const Args &
     constexpr int VEC = 16 / sizeof(T);
     const int pieces = (a.V + VEC - 1) / VEC;
     constexpr int FIT = 100 * 1024 / 16, CACHED = 48 * 1024 / 16;
-    // blocks of a cluster: what shared memory asks for, and more while there
-    // are multiprocessors without a row and 8 KB for each block
+    // blocks of a cluster: what keeps the rows in work within half of the L2,
+    // for the second pass, and more while there are multiprocessors without a
+    // row and 4 KB for each block
     int ranks = 1;
     while (ranks < 8 && (pieces > ranks * FIT || (a.n * ranks * 2 <= SMS && pieces >= ranks * 2 * LONG_THREADS)))
         ranks *= 2;
