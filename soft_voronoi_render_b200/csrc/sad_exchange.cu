@@ -131,7 +131,7 @@ template <int VEC, bool ROW_PER_BLOCK> struct Lanes {
 };
 
 // writes the dot products of the group's row; dot[k] of empty slots is 0
-template <bool ROW_PER_BLOCK>
+template <bool FULL, bool ROW_PER_BLOCK>
 __device__ __forceinline__ void finish_dots(float (&dot)[K_MAX], int L, int lane, long long t, bool in, int K,
                                             float *__restrict__ dots) {
     int first, count;
@@ -151,9 +151,17 @@ __device__ __forceinline__ void finish_dots(float (&dot)[K_MAX], int L, int lane
     }
     // of the lanes that hold the same sum (L > 8) the first writes
     if (!in || (L > 8 && (lane & (L / 8 - 1)))) return;
+    if constexpr (FULL) {  // 32 bytes a row, aligned
+        float *to = dots + t * K_MAX + first;
+        if (count == 1) *to = dot[0];
+        else if (count == 2) *reinterpret_cast<float2 *>(to) = make_float2(dot[0], dot[1]);
+        else *reinterpret_cast<float4 *>(to) = make_float4(dot[0], dot[1], dot[2], dot[3]);
+        if (count == 8) *reinterpret_cast<float4 *>(to + 4) = make_float4(dot[4], dot[5], dot[6], dot[7]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < K_MAX; ++i)
-        if (i < count && first + i < K) dots[t * K + first + i] = dot[i];
+        for (int i = 0; i < K_MAX; ++i)
+            if (i < count && first + i < K) dots[t * K + first + i] = dot[i];
+    }
 }
 
 // Empty slots are rows of zeros with weight 0, so that nothing branches
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, SUM && DOT ? 3 : 4) gather_kernel(con
             both(dots2[k], dot[k], other);
             dot[k] = id[k] < n_at ? dot[k] + other : 0.0f;  // G may hold infinities
         }
-        finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
+        finish_dots<FULL, ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
     }
 }
 
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
     if (DOT) {
 #pragma unroll
         for (int k = 0; k < K_MAX; ++k) dot[k] = id[k] < n_at ? dot[k] : 0.0f;
-        finish_dots<ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
+        finish_dots<FULL, ROW_PER_BLOCK>(dot, me.L, me.lane, me.t, me.in, K, dots);
     }
 }
 
@@ -639,7 +647,7 @@ cudaError_t gather(RowsIn rows, const int32_t *at, long long n_at, const float *
     T *o = static_cast<T *>(out.p);
     const Shape s = shape_of(n, D, VEC);
     const uint32_t m = (uint32_t)n_at;
-    const bool full = K == K_MAX && aligned16(at) && aligned16(w);
+    const bool full = K == K_MAX && aligned16(at) && aligned16(w) && aligned16(dots);
     if (o && dots) {
         if (full) gather_launch<T, VEC, true, true, true>(s, r, rows.ld, at, m, w, g, other.ld, n, K, D, o, out.ld, dots, st);
         else gather_launch<T, VEC, false, true, true>(s, r, rows.ld, at, m, w, g, other.ld, n, K, D, o, out.ld, dots, st);
@@ -673,7 +681,7 @@ cudaError_t spread(RowsIn x, const int32_t *at, long long n_at, const float *w, 
     T *o = static_cast<T *>(to.p);
     const Shape s = shape_of(n, D, VEC);
     const uint32_t m = (uint32_t)n_at;
-    const bool full = K == K_MAX && aligned16(at) && aligned16(w);
+    const bool full = K == K_MAX && aligned16(at) && aligned16(w) && aligned16(dots);
     if (dots) {
         if (full) spread_launch<T, VEC, true, true>(s, xp, x.ld, at, m, w, r, rows.ld, n, K, D, o, to.ld, dots, st);
         else spread_launch<T, VEC, false, true>(s, xp, x.ld, at, m, w, r, rows.ld, n, K, D, o, to.ld, dots, st);

@@ -63,6 +63,7 @@ Plan make_plan(long long n, int E) {
     return p;
 }
 
+size_t move_shared(int D) { return (size_t)D * (sizeof(uint32_t) + WARPS * sizeof(uint16_t)); }
 size_t up(size_t v) { return (v + 255) & ~size_t(255); }
 
 __device__ __forceinline__ uint32_t key_of(int32_t id, int E) {
@@ -154,7 +155,7 @@ __device__ void digit_bases(const uint32_t *__restrict__ totals, int D, uint32_t
 
 // moves every item to its digit's place.  The first pass reads ids (the pair
 // is the index); the last writes order and place instead of keys and pairs.
-__global__ void __launch_bounds__(THREADS) move_kernel(const int32_t *__restrict__ ids,
+__global__ void __launch_bounds__(THREADS, 4) move_kernel(const int32_t *__restrict__ ids,
                                                        const uint32_t *__restrict__ keys,
                                                        const uint32_t *__restrict__ pairs, long long n, int E,
                                                        long long per_block, int shift, int bits,
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(THREADS) move_kernel(const int32_t *__restrict
     __shared__ uint32_t warp_sum[WARPS];
     const int D = 1 << bits;
     uint32_t *base = smem;            // [D] next global position of each digit
-    uint32_t *wc = smem + D;          // [WARPS][D] counts, then starts, of each warp's items
+    uint16_t *wc = reinterpret_cast<uint16_t *>(smem + D);  // [WARPS][D] counts, then starts in the tile
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     digit_bases(totals, D, base, warp_sum);
     // one pass sorts on the whole key: the digits' bases are the offsets
@@ -180,43 +181,54 @@ __global__ void __launch_bounds__(THREADS) move_kernel(const int32_t *__restrict
     for (int d = threadIdx.x; d < D; d += THREADS) base[d] += counts[(size_t)d * gridDim.x + blockIdx.x];
     const long long lo = blockIdx.x * per_block, hi = min(n, lo + per_block);
     for (long long t0 = lo; t0 < hi; t0 += TILE) {
-        for (int d = threadIdx.x; d < D * WARPS; d += THREADS) wc[d] = 0;
-        __syncthreads();
+        uint16_t *mine = wc + warp * D;
+        for (int d = lane; d < D / 2; d += 32) reinterpret_cast<uint32_t *>(mine)[d] = 0;
+        __syncwarp();
         uint32_t key[ITEMS], pair[ITEMS], rank[ITEMS];
-        uint32_t *mine = wc + warp * D;
 #pragma unroll
         for (int q = 0; q < ITEMS; ++q) {
             const long long i = t0 + warp * (32 * ITEMS) + q * 32 + lane;
             const bool in = i < hi;
             key[q] = in ? (keys ? keys[i] : key_of(ids[i], E)) : 0xffffffffu;
             pair[q] = in ? (pairs ? pairs[i] : (uint32_t)i) : 0;
+        }
+#pragma unroll
+        for (int q = 0; q < ITEMS; ++q) {
+            const long long i = t0 + warp * (32 * ITEMS) + q * 32 + lane;
+            const bool in = i < hi;
             const uint32_t d = key[q] >> shift & (D - 1);
             const unsigned peers = __match_any_sync(0xffffffffu, in ? d : 0xffffffffu);
             const unsigned below = peers & ((1u << lane) - 1);
             uint32_t old = 0;
             if (in) old = mine[d];
             __syncwarp();
-            if (in && below == 0) mine[d] = old + __popc(peers);
+            if (in && below == 0) mine[d] = (uint16_t)(old + __popc(peers));
             __syncwarp();
             rank[q] = old + __popc(below);
         }
         __syncthreads();
-        // the warps' starts within the digit; the tile's items move its base on
-        for (int d = threadIdx.x; d < D; d += THREADS) {
-            uint32_t s = base[d];
+        // the warps' starts among the tile's items of a digit, two digits at a time
+        uint32_t total[(1 << MAX_BITS) / (2 * THREADS)];
+#pragma unroll
+        for (int u = 0; u < (1 << MAX_BITS) / (2 * THREADS); ++u) {
+            const int d = 2 * threadIdx.x + u * 2 * THREADS;
+            if (d >= D) break;
+            uint32_t at = 0;
+#pragma unroll
             for (int w = 0; w < WARPS; ++w) {
-                const uint32_t c = wc[w * D + d];
-                wc[w * D + d] = s;
-                s += c;
+                uint32_t *c = reinterpret_cast<uint32_t *>(wc + w * D + d);
+                const uint32_t add = *c;
+                *c = at;
+                at += add;
             }
-            base[d] = s;
+            total[u] = at;
         }
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < ITEMS; ++q) {
             const long long i = t0 + warp * (32 * ITEMS) + q * 32 + lane;
             if (i >= hi) continue;
-            const uint32_t pos = mine[key[q] >> shift & (D - 1)] + rank[q];
+            const uint32_t d = key[q] >> shift & (D - 1), pos = base[d] + mine[d] + rank[q];
             if (order) {
                 const bool empty = key[q] == (uint32_t)E;
                 order[pos] = empty ? -1 : (int32_t)pair[q];
@@ -227,6 +239,13 @@ __global__ void __launch_bounds__(THREADS) move_kernel(const int32_t *__restrict
             }
         }
         __syncthreads();
+#pragma unroll
+        for (int u = 0; u < (1 << MAX_BITS) / (2 * THREADS); ++u) {
+            const int d = 2 * threadIdx.x + u * 2 * THREADS;
+            if (d >= D) break;
+            base[d] += total[u] & 0xffffu;
+            base[d + 1] += total[u] >> 16;
+        }
     }
 }
 
@@ -268,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 4) tile_sort_kernel(const int32_t *__
     __shared__ uint32_t word[WORDS], before[WORDS];
     const int D = 1 << bits;
     uint32_t *items = smem;                                           // [RUN_TILE]
-    uint16_t *wc = reinterpret_cast<uint16_t *>(smem + RUN_TILE);     // [WARPS][D]
+    uint16_t *wc = reinterpret_cast<uint16_t *>(smem + RUN_TILE);     // [WARPS][D], then [RUN_TILE]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long t0 = (long long)blockIdx.x * RUN_TILE;
     const int count = (int)min((long long)RUN_TILE, n - t0);
@@ -377,25 +396,18 @@ __global__ void __launch_bounds__(THREADS, 4) tile_sort_kernel(const int32_t *__
         heads[(size_t)blockIdx.x * WORDS + threadIdx.x] = word[threadIdx.x];
         heads_before[(size_t)blockIdx.x * WORDS + threadIdx.x] = (uint16_t)before[threadIdx.x];
     }
+    uint16_t *starts = wc;  // [runs]: the counters are done with
 #pragma unroll
     for (int q = 0; q < RUN_ITEMS; ++q) {
-        const int p = p0 + 32 * q;
-        const uint32_t b = word[p >> 5];
-        if (!(b >> lane & 1u)) continue;
-        const uint32_t r = before[p >> 5] + __popc(b & ((1u << lane) - 1));
-        // the next head, in this word or a later one
-        const uint32_t rest = lane < 31 ? b >> (lane + 1) : 0;
-        int end = count;
-        if (rest) {
-            end = p + __ffs(rest);
-        } else {
-            for (int v = (p >> 5) + 1; v < WORDS; ++v)
-                if (word[v]) {
-                    end = v * 32 + __ffs(word[v]) - 1;
-                    break;
-                }
-        }
-        run_word[t0 + r] = (item[q] & ~(uint32_t)(RUN_TILE - 1)) | (uint32_t)(end - p - 1);
+        const int w = warp * RUN_ITEMS + q;
+        const uint32_t b = word[w];
+        if (b >> lane & 1u) starts[before[w] + __popc(b & ((1u << lane) - 1))] = (uint16_t)(32 * w + lane);
+    }
+    __syncthreads();
+    const int runs = (int)(before[WORDS - 1] + __popc(word[WORDS - 1]));
+    for (int r = threadIdx.x; r < runs; r += THREADS) {
+        const int p = starts[r], end = r + 1 < runs ? starts[r + 1] : count;
+        run_word[t0 + r] = (items[p] & ~(uint32_t)(RUN_TILE - 1)) | (uint32_t)(end - p - 1);
         run_start[t0 + r] = (uint16_t)p;
     }
 }
@@ -538,45 +550,61 @@ __global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__
     offsets[e] = (int32_t)(lo < total ? sorted[lo] : (uint32_t)n);
 }
 
-// a tile's part of order and place
-__global__ void __launch_bounds__(THREADS) tile_write_kernel(long long n, const uint16_t *__restrict__ local,
-                                                             const uint32_t *__restrict__ heads,
-                                                             const uint16_t *__restrict__ heads_before,
-                                                             const uint32_t *__restrict__ where,
-                                                             const uint16_t *__restrict__ run_start,
-                                                             const uint32_t *__restrict__ run_count,
-                                                             const int32_t *__restrict__ offsets, int E,
-                                                             int32_t *__restrict__ order, int32_t *__restrict__ place) {
-    __shared__ uint32_t shift[RUN_TILE];   // position less place in the tile, of each run
-    __shared__ int32_t out[RUN_TILE];
+// a tile's part of order and place; FULL: a tile of RUN_TILE pairs
+template <bool FULL>
+__device__ __forceinline__ void tile_write(int count, uint32_t t0, const uint16_t (&idx)[RUN_ITEMS], uint32_t words,
+                                           uint32_t befores, uint32_t live, const uint32_t *shift, int32_t *out,
+                                           int32_t *__restrict__ order, int32_t *__restrict__ place) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long t0 = (long long)blockIdx.x * RUN_TILE;
-    const int count = (int)min((long long)RUN_TILE, n - t0);
-    const uint32_t runs = run_count[blockIdx.x];
-    // everything is loaded before the first wait
-    uint16_t idx[RUN_ITEMS];
-    uint32_t word[RUN_ITEMS], before[RUN_ITEMS];
 #pragma unroll
     for (int q = 0; q < RUN_ITEMS; ++q) {
-        const int w = warp * RUN_ITEMS + q, p = 32 * w + lane;
-        idx[q] = p < count ? local[t0 + p] : 0;
-        word[q] = __ldg(heads + (size_t)blockIdx.x * WORDS + w);
-        before[q] = __ldg(heads_before + (size_t)blockIdx.x * WORDS + w);
-    }
-    const uint32_t live = (uint32_t)__ldg(offsets + E);  // positions from here on are empty slots
-    for (uint32_t r = threadIdx.x; r < runs; r += THREADS) shift[r] = where[t0 + r] - run_start[t0 + r];
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < RUN_ITEMS; ++q) {
+        const uint32_t word = __shfl_sync(0xffffffffu, words, q), before = __shfl_sync(0xffffffffu, befores, q);
         const int p = warp * (32 * RUN_ITEMS) + 32 * q + lane;
-        if (p >= count) continue;
-        const uint32_t pos = shift[before[q] + __popc(word[q] & (0xffffffffu >> (31 - lane))) - 1] + p;
+        if (!FULL && p >= count) continue;
+        const uint32_t pos = shift[before + __popc(word & (0xffffffffu >> (31 - lane))) - 1] + p;
         const bool empty = pos >= live;
         order[pos] = empty ? -1 : (int32_t)(t0 + idx[q]);
         out[idx[q]] = empty ? -1 : (int32_t)pos;
     }
     __syncthreads();
-    for (int p = threadIdx.x; p < count; p += THREADS) place[t0 + p] = out[p];
+    place += t0;
+    if (FULL && (reinterpret_cast<uintptr_t>(place) & 15) == 0) {
+#pragma unroll
+        for (int q = 0; q < RUN_ITEMS / 4; ++q)
+            reinterpret_cast<int4 *>(place)[q * THREADS + threadIdx.x] = reinterpret_cast<const int4 *>(out)[q * THREADS + threadIdx.x];
+    } else {
+        for (int p = threadIdx.x; p < count; p += THREADS) place[p] = out[p];
+    }
+}
+__global__ void __launch_bounds__(THREADS, 6) tile_write_kernel(long long n, const uint16_t *__restrict__ local,
+                                                                const uint32_t *__restrict__ heads,
+                                                                const uint16_t *__restrict__ heads_before,
+                                                                const uint32_t *__restrict__ where,
+                                                                const uint16_t *__restrict__ run_start,
+                                                                const uint32_t *__restrict__ run_count,
+                                                                const int32_t *__restrict__ offsets, int E,
+                                                                int32_t *__restrict__ order,
+                                                                int32_t *__restrict__ place) {
+    __shared__ uint32_t shift[RUN_TILE];   // position less place in the tile, of each run
+    __shared__ __align__(16) int32_t out[RUN_TILE];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t0 = (long long)blockIdx.x * RUN_TILE;
+    const int count = (int)min((long long)RUN_TILE, n - t0);
+    const uint32_t runs = run_count[blockIdx.x];
+    // everything is loaded before the first wait; lane q has the q-th word of heads
+    uint16_t idx[RUN_ITEMS];
+#pragma unroll
+    for (int q = 0; q < RUN_ITEMS; ++q) {
+        const int p = warp * (32 * RUN_ITEMS) + 32 * q + lane;
+        idx[q] = p < count ? local[t0 + p] : 0;
+    }
+    const size_t w = (size_t)blockIdx.x * WORDS + warp * RUN_ITEMS + (lane & (RUN_ITEMS - 1));
+    const uint32_t words = __ldg(heads + w), befores = __ldg(heads_before + w);
+    const uint32_t live = (uint32_t)__ldg(offsets + E);  // positions from here on are empty slots
+    for (uint32_t r = threadIdx.x; r < runs; r += THREADS) shift[r] = where[t0 + r] - run_start[t0 + r];
+    __syncthreads();
+    if (count == RUN_TILE) tile_write<true>(count, (uint32_t)t0, idx, words, befores, live, shift, out, order, place);
+    else tile_write<false>(count, (uint32_t)t0, idx, words, befores, live, shift, out, order, place);
 }
 
 // workspace of the sort by runs
@@ -616,7 +644,7 @@ cudaError_t route_by_runs(const int32_t *ids, long long n, int E, const Plan &p,
     const RunSpace s(ws, n, p);
     const int D = 1 << p.bits;
     const uint32_t *length = s.base + s.tiles;
-    const size_t sort_shared = RUN_TILE * sizeof(uint32_t) + (size_t)WARPS * D * sizeof(uint16_t);
+    const size_t sort_shared = RUN_TILE * sizeof(uint32_t) + (size_t)(WARPS * D > RUN_TILE ? WARPS * D : RUN_TILE) * sizeof(uint16_t);
     tile_sort_kernel<<<s.tiles, THREADS, sort_shared, st>>>(ids, n, E, p.passes, p.bits, s.local, s.heads,
                                                             s.heads_before, s.run_word, s.run_start, s.run_count);
     run_base_kernel<<<1, 1024, 0, st>>>(s.run_count, s.tiles, s.base);
@@ -628,7 +656,7 @@ cudaError_t route_by_runs(const int32_t *ids, long long n, int E, const Plan &p,
         count_kernel<<<RUN_BLOCKS, THREADS, D * sizeof(uint32_t), st>>>(nullptr, from[0], slots, E, 0, shift, p.bits,
                                                                         s.counts, length);
         scan_kernel<<<D, THREADS, 0, st>>>(s.counts, RUN_BLOCKS, s.totals);
-        move_kernel<<<RUN_BLOCKS, THREADS, (size_t)D * (1 + WARPS) * sizeof(uint32_t), st>>>(
+        move_kernel<<<RUN_BLOCKS, THREADS, move_shared(D), st>>>(
             nullptr, from[0], from[1], slots, E, 0, shift, p.bits, s.counts, s.totals, to[0], to[1], nullptr, nullptr,
             nullptr, length);
     }
@@ -730,7 +758,7 @@ cudaError_t launch_route(const int32_t *ids, long long n_rows, int K, int E, int
                                                                       counts, nullptr);
         scan_kernel<<<D, THREADS, 0, st>>>(counts, p.blocks, totals);
         uint32_t *ko = last ? nullptr : buf[q & 1][0], *po = last ? nullptr : buf[q & 1][1];
-        move_kernel<<<p.blocks, THREADS, (size_t)D * (1 + WARPS) * sizeof(uint32_t), st>>>(
+        move_kernel<<<p.blocks, THREADS, move_shared(D), st>>>(
             ids, keys, pairs, n, E, p.per_block, shift, p.bits, counts, totals, ko, po, last ? order : nullptr,
             last ? place : nullptr, last && p.passes == 1 ? offsets : nullptr, nullptr);
         keys = ko;
