@@ -463,6 +463,19 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
         }
         copies_end_group();
     };
+    // gamma stays in registers where there are enough: read again for every row
+    // it is most of what goes through the L1
+    constexpr bool KEEP = NV * VEC <= 16;
+    float kept[KEEP ? NV * VEC : 1];
+    if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float gm[VEC];
+            load_param<VEC>(gamma, min(i * (int)blockDim.x + (int)threadIdx.x, pieces - 1) * VEC, 1.0f, gm);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) kept[i * VEC + q] = gm[q];
+        }
+    }
     float m_next[ROWS], rs_next[ROWS];
     auto fetch_stats = [&](long long r) {
 #pragma unroll
@@ -490,7 +503,12 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
             const int c = min(i * (int)blockDim.x + (int)threadIdx.x, pieces - 1);
             const bool in = i < NV - 1 || i * (int)blockDim.x + (int)threadIdx.x < pieces;
             float gm[VEC];
-            load_param<VEC>(gamma, c * VEC, 1.0f, gm);
+            if (KEEP) {
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) gm[q] = kept[i * VEC + q];
+            } else {
+                load_param<VEC>(gamma, c * VEC, 1.0f, gm);
+            }
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
                 g[j].p[i].clear();
@@ -525,7 +543,12 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
             const int c = min(i * (int)blockDim.x + (int)threadIdx.x, pieces - 1);
             const bool in = i < NV - 1 || i * (int)blockDim.x + (int)threadIdx.x < pieces;
             float gm[VEC];
-            load_param<VEC>(gamma, c * VEC, 1.0f, gm);
+            if (KEEP) {
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) gm[q] = kept[i * VEC + q];
+            } else {
+                load_param<VEC>(gamma, c * VEC, 1.0f, gm);
+            }
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
                 const float a = all[2 * j] * inv, b = all[2 * j + 1] * inv;
