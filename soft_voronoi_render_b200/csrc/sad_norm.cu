@@ -382,28 +382,36 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, 
     for (int j = 0; j < ROWS; ++j) row[j].load(x + (r0 + j) * ldx, c0, step, r0 + j < n ? D : 0);
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
-        s[j] = 0.0f;
+        Two sum = two(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) s[j] += row[j].p[i].get(q);
+            for (int q = 0; q < VEC; q += 2) sum = add_two(sum, pair_at(row[j].p[i], q));
         }
+        float other;
+        both(sum, s[j], other);
+        s[j] += other;
     }
     block_sums<ROWS>(s, scratch[0], m);
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
         row[j].stay_packed();
         m[j] /= (float)D;
-        s[j] = 0.0f;
+        Two sum = two(0.0f, 0.0f);
+        const Two mm = two(-m[j], -m[j]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = i < NV - 1 || c0 + i * step < D;
+            Two part = sum;
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                const float d = in ? row[j].p[i].get(q) - m[j] : 0.0f;
-                s[j] = fmaf(d, d, s[j]);
+            for (int q = 0; q < VEC; q += 2) {
+                const Two d = add_two(pair_at(row[j].p[i], q), mm);
+                part = fma_two(d, d, part);
             }
+            if (i < NV - 1 || c0 + i * step < D) sum = part;
         }
+        float other;
+        both(sum, s[j], other);
+        s[j] += other;
     }
     block_sums<ROWS>(s, scratch[1], rs);
 #pragma unroll
@@ -421,8 +429,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, 
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
             float f[VEC];
+            const Two mm = two(-m[j], -m[j]), rr = two(rs[j], rs[j]);
 #pragma unroll
-            for (int q = 0; q < VEC; ++q) f[q] = fmaf((row[j].p[i].get(q) - m[j]) * rs[j], g[q], b[q]);
+            for (int q = 0; q < VEC; q += 2)
+                both(fma_two(mul_two(add_two(pair_at(row[j].p[i], q), mm), rr), two(g[q], g[q + 1]), two(b[q], b[q + 1])),
+                     f[q], f[q + 1]);
             Pack<T, VEC> o;
             o.set(f);
             if (in && r0 + j < n) store_pack<T, VEC>(y + (r0 + j) * ldy + c, o);
@@ -452,7 +463,9 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
     const long long stride = (long long)gridDim.x * ROWS;
     const float inv = 1.0f / (float)D;
     R ring{ring_base};
-    float dg[SUMS ? NV * VEC : 1] = {}, db[SUMS ? NV * VEC : 1] = {};
+    Two dg[SUMS ? NV * VEC / 2 : 1], db[SUMS ? NV * VEC / 2 : 1];
+#pragma unroll
+    for (int i = 0; i < (SUMS ? NV * VEC / 2 : 1); ++i) dg[i] = db[i] = two(0.0f, 0.0f);
     auto fetch = [&](int s, long long r) {
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
@@ -491,13 +504,14 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
     for (int turn = 0; r < n; r += stride, turn ^= 1) {
         fetch(ring.slot ? ring.slot - 1 : R::STAGES - 1, r + (R::STAGES - 1) * stride);
         float m[ROWS], rs[ROWS], sums[2 * ROWS], all[2 * ROWS];
+        Two pairs[2 * ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) m[j] = m_next[j], rs[j] = rs_next[j];
         fetch_stats(r + stride);
         copies_wait<R::STAGES - 1>();
         RowPart<T, VEC, NV> g[ROWS], h[ROWS];
 #pragma unroll
-        for (int j = 0; j < 2 * ROWS; ++j) sums[j] = 0.0f;
+        for (int j = 0; j < 2 * ROWS; ++j) pairs[j] = two(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = min(i * (int)blockDim.x + (int)threadIdx.x, pieces - 1);
@@ -517,20 +531,28 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
                     g[j].p[i] = ring.get(2 * j, i);
                     h[j].p[i] = ring.get(2 * j + 1, i);
                 }
+                const Two mm = two(-m[j], -m[j]), rr = two(rs[j], rs[j]);
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    const int k = i * VEC + q;
-                    const float hk = (h[j].p[i].get(q) - m[j]) * rs[j], dk = g[j].p[i].get(q);
+                for (int q = 0; q < VEC; q += 2) {
+                    const int k = (i * VEC + q) / 2;
+                    const Two hk = mul_two(add_two(pair_at(h[j].p[i], q), mm), rr), dk = pair_at(g[j].p[i], q);
                     if (SUMS) {
-                        dg[k] = fmaf(dk, hk, dg[k]);
-                        db[k] += dk;
+                        dg[k] = fma_two(dk, hk, dg[k]);
+                        db[k] = add_two(db[k], dk);
                     }
-                    sums[2 * j] = fmaf(dk, gm[q], sums[2 * j]);
-                    sums[2 * j + 1] = fmaf(__fmul_rn(dk, gm[q]), hk, sums[2 * j + 1]);
+                    const Two gk = mul_two(dk, two(gm[q], gm[q + 1]));
+                    pairs[2 * j] = add_two(pairs[2 * j], gk);
+                    pairs[2 * j + 1] = fma_two(gk, hk, pairs[2 * j + 1]);
                 }
             }
         }
         ring.next();
+#pragma unroll
+        for (int j = 0; j < 2 * ROWS; ++j) {
+            float other;
+            both(pairs[j], sums[j], other);
+            sums[j] += other;
+        }
         // two sets of scratch in turn: one barrier a step
         block_sums<2 * ROWS>(sums, scratch[turn], all);
 #pragma unroll
@@ -553,10 +575,12 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
             for (int j = 0; j < ROWS; ++j) {
                 const float a = all[2 * j] * inv, b = all[2 * j + 1] * inv;
                 float f[VEC];
+                const Two mm = two(-m[j], -m[j]), rr = two(rs[j], rs[j]), aa = two(-a, -a), bb = two(-b, -b);
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    const float hk = (h[j].p[i].get(q) - m[j]) * rs[j];
-                    f[q] = rs[j] * fmaf(g[j].p[i].get(q), gm[q], -fmaf(hk, b, a));
+                for (int q = 0; q < VEC; q += 2) {
+                    const Two hk = mul_two(add_two(pair_at(h[j].p[i], q), mm), rr);
+                    const Two gk = fma_two(pair_at(g[j].p[i], q), two(gm[q], gm[q + 1]), fma_two(hk, bb, aa));
+                    both(mul_two(rr, gk), f[q], f[q + 1]);
                 }
                 Pack<T, VEC> o;
                 o.set(f);
@@ -571,9 +595,10 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
         const int c = i * blockDim.x + threadIdx.x;
         if (c >= pieces) break;
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-            out[c * VEC + q] = dg[i * VEC + q];
-            out[D + c * VEC + q] = db[i * VEC + q];
+        for (int q = 0; q < VEC; q += 2) {
+            const int k = (i * VEC + q) / 2;
+            both(dg[k], out[c * VEC + q], out[c * VEC + q + 1]);
+            both(db[k], out[D + c * VEC + q], out[D + c * VEC + q + 1]);
         }
     }
 }

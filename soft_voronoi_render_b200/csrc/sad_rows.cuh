@@ -97,6 +97,9 @@ __device__ __forceinline__ Two mul_two(Two a, Two b) {
     return r;
 }
 
+// elements i and i + 1 of a piece
+template <typename P> __device__ __forceinline__ Two pair_at(const P &p, int i) { return two(p.get(i), p.get(i + 1)); }
+
 // sum over the L (a power of two, at most 32) neighbouring lanes of a group,
 // the same bits in every lane
 template <int L> __device__ __forceinline__ float group_sum(float v) {
