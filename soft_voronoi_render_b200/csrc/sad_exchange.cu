@@ -486,6 +486,11 @@ __device__ __forceinline__ size_t piece_row(uint32_t from, uint32_t k, uint32_t 
     return k ? 2 * ((size_t)(from / C) + k) : 2 * (size_t)(from / C) + 1;
 }
 
+// (none where the offsets do not ascend, as those of a route do)
+__device__ __forceinline__ uint32_t pieces_of(uint32_t from, uint32_t end, uint32_t C) {
+    return end > from ? (end - from + C - 1) / C : 0;
+}
+
 // The order in which pieces are taken: a count of each part of the rows, its
 // scan, and the pieces put into their part's places.  `per` experts a block:
 // fewer where few experts have many pieces.
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(THREADS) turn_kernel(const int32_t *__restrict
     uint32_t from = 0, pieces = 0;
     if (threadIdx.x < per && e < E) {
         from = min((uint32_t)__ldg(offsets + e), n);
-        pieces = (min((uint32_t)__ldg(offsets + e + 1), n) - from + C - 1) / C;
+        pieces = pieces_of(from, min((uint32_t)__ldg(offsets + e + 1), n), C);
     }
     auto put = [&](uint32_t expert, uint32_t a, uint32_t k) {
         const uint32_t at = a + k * C;
@@ -555,6 +560,7 @@ __global__ void __launch_bounds__(THREADS, 4) piece_kernel(const T *__restrict__
     const uint2 piece = __ldg(turn + t);
     if (piece.x >= (uint32_t)E) return;
     const uint32_t from = min((uint32_t)__ldg(offsets + piece.x), n), end = min((uint32_t)__ldg(offsets + piece.x + 1), n);
+    if (piece.y >= pieces_of(from, end, C)) return;
     const uint32_t a = from + piece.y * C, b = min(a + C, end);
     const bool whole = end - from <= C;
     for (int slab = blockIdx.y * 32 * VEC; slab < D; slab += gridDim.y * 32 * VEC) {
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(THREADS) piece_join_kernel(const int32_t *__re
     uint32_t from = 0, pieces = 0;
     if (threadIdx.x < per && e < E) {
         from = min((uint32_t)__ldg(offsets + e), n);
-        pieces = (min((uint32_t)__ldg(offsets + e + 1), n) - from + C - 1) / C;
+        pieces = pieces_of(from, min((uint32_t)__ldg(offsets + e + 1), n), C);
     }
     s_from[threadIdx.x] = from;
     s_pieces[threadIdx.x] = pieces;

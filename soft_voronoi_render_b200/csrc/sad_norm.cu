@@ -675,13 +675,17 @@ void forward_shape(const Shape &s, RowsIn x, const float *gamma, const float *be
                                                                                  s.log_l, yp, y.ld, mean, rstd);
 }
 
-// blocks of a kernel that takes rows in turn: all that stay resident, at most
-// one a row and `most`
-template <typename F> int resident_blocks(F kernel, int threads, size_t shared, long long rows, long long most) {
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, shared) != cudaSuccess || per_sm < 1)
-        per_sm = 1;
-    return (int)min(min(rows, most), (long long)SMS * per_sm);
+// blocks of a kernel that takes rows in turn: all that stay resident by its
+// registers, at most one a row and `most`
+int resident_blocks(int registers, int threads, size_t shared, long long rows, long long most) {
+    const int warps = threads / 32;
+    int per_sm = min(64 / warps, 65536 / ((registers + 7) / 8 * 8 * 32 * warps));
+    per_sm = min(per_sm, (int)(227 * 1024 / (shared + 2048)));  // 1 KB of the system's, and the static arrays
+    return (int)min(min(rows, most), (long long)SMS * max(per_sm, 1));
+}
+template <typename F> int registers_of(F kernel) {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 128;
 }
 
 // wide rows: pieces a thread, two or what 512 threads need
@@ -751,7 +755,9 @@ int backward_shape(const Shape &s, RowsIn dy, RowsIn x, const float *gamma, cons
     const T *dyp = static_cast<const T *>(dy.p), *xp = static_cast<const T *>(x.p);
     auto kernel = partial ? norm_backward_kernel<T, VEC, NV, BLOCK, true> : norm_backward_kernel<T, VEC, NV, BLOCK, false>;
     const size_t shared = partial && !BLOCK ? sizeof(float) * (THREADS / 32) * D : 0;
-    const int blocks = resident_blocks(kernel, s.threads, shared, s.blocks, backward_blocks(D));
+    static const int registers[2] = {registers_of(norm_backward_kernel<T, VEC, NV, BLOCK, false>),
+                                     registers_of(norm_backward_kernel<T, VEC, NV, BLOCK, true>)};
+    const int blocks = resident_blocks(registers[partial != nullptr], s.threads, shared, s.blocks, backward_blocks(D));
     kernel<<<blocks, s.threads, shared, st>>>(dyp, dy.ld, xp, x.ld, gamma, mean, rstd, n, D, s.log_l,
                                               static_cast<T *>(dx.p), dx.ld, partial);
     return blocks;
@@ -766,7 +772,10 @@ int backward_wide(RowsIn dy, RowsIn x, const float *gamma, const float *mean, co
     auto kernel = partial ? norm_wide_backward_kernel<T, NV, ROWS, true> : norm_wide_backward_kernel<T, NV, ROWS, false>;
     e = allow_shared(kernel, shared);
     if (e != cudaSuccess) return 0;
-    const int blocks = resident_blocks(kernel, threads, shared, (n + ROWS - 1) / ROWS, backward_blocks(D));
+    static const int registers[2] = {registers_of(norm_wide_backward_kernel<T, NV, ROWS, false>),
+                                     registers_of(norm_wide_backward_kernel<T, NV, ROWS, true>)};
+    const int blocks = resident_blocks(registers[partial != nullptr], threads, shared, (n + ROWS - 1) / ROWS,
+                                       backward_blocks(D));
     kernel<<<blocks, threads, shared, st>>>(static_cast<const T *>(dy.p), dy.ld, static_cast<const T *>(x.p), x.ld,
                                             gamma, mean, rstd, n, D, static_cast<T *>(dx.p), dx.ld, partial);
     return blocks;

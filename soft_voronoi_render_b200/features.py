@@ -13,6 +13,8 @@ outside [0, n_sites) is an empty slot; weights are dense float32.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -75,6 +77,11 @@ def _run(device, call, *args):
 
 def _at(x):
     return None if x is None else x.data_ptr()
+
+
+# workspace sizes are functions of the sizes alone
+_blend_bytes = functools.lru_cache(256)(_lib.sad_blend_workspace_bytes)
+_norm_bytes = functools.lru_cache(256)(_lib.sad_layer_norm_workspace_bytes)
 
 
 class Route:
@@ -247,7 +254,7 @@ def blend_backward(dout, F, ids, weights, route=None, dF=None):
             dF = weights.new_empty((E, D))
         else:
             _dense("dF", dF, torch.float32, (E, D), dev)
-        nbytes = _lib.sad_blend_workspace_bytes(T, K, E, D)
+        nbytes = _blend_bytes(T, K, E, D)
         ws = weights.new_empty(-(-nbytes // 4))
     elif dF is not None:
         _refuse("dF needs a route")
@@ -297,7 +304,7 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, want_affine: bool = True, dx=N
     nbytes = 0
     if want_affine:
         dgamma, dbeta = mean.new_empty(D), mean.new_empty(D)
-        nbytes = _lib.sad_layer_norm_workspace_bytes(T, D)
+        nbytes = _norm_bytes(T, D)
         ws = mean.new_empty(-(-nbytes // 4))
     _run(dev, _lib.load().sad_layer_norm_backward, _TYPES[x.dtype], dy.data_ptr(), ld, x.data_ptr(), ldx, _at(gamma),
          mean.data_ptr(), rstd.data_ptr(), T, D, dx.data_ptr(), lddx, _at(dgamma), _at(dbeta), _at(ws), nbytes)

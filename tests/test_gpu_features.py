@@ -707,3 +707,95 @@ def test_route_of_many_pairs(T, K, E, kind):
     assert torch.equal(r.order.long(), torch.where(pos < m, perm, -1))
     assert torch.equal(r.place.view(-1).long(), torch.where(key < E, place, -1))
     assert torch.equal(r.offsets.long(), torch.searchsorted(skey, torch.arange(E + 1, device="cuda")))
+
+
+def _graphed(call):
+    """call() captured and replayed twice after its inputs were put back."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()  # set-up outside the capture
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    return out
+
+
+def test_captured_large_forms():
+    """The forms for large sizes replay to the eager bits: clusters of a long
+    row, the sort by runs, segment sums of far rows, wide rows' norm."""
+    f = feat()
+    g = rng(21)
+    z, tid, tl = randn(g, 2, 90001), torch.randint(0, 90001, (2, 9), generator=g, device="cuda").int(), randn(g, 2, 9)
+    want = f.distill(z, tid, tl)
+    got = _graphed(lambda: f.distill(z, tid, tl))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    T, E, D = 300000, 5000, 64
+    ids = ((torch.arange(T * 8, device="cuda") // 50 * 77 + torch.randint(0, 5, (T * 8,), generator=g, device="cuda"))
+           % E).int().view(T, 8).contiguous()
+    w = torch.rand((T, 8), generator=g, device="cuda")
+    F, dout = randn(g, E, D), randn(g, T, D)
+    r, r2 = f.Route(T, 8, E).build(ids), f.Route(T, 8, E)
+    want = f.blend_backward(dout, F, ids, w, r)
+    got = _graphed(lambda: f.blend_backward(dout, F, ids, w, r2.build(ids)))
+    assert torch.equal(r.order, r2.order) and torch.equal(r.place, r2.place) and torch.equal(r.offsets, r2.offsets)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    x, dy = randn(g, 900, 4096, dtype=torch.bfloat16), randn(g, 900, 4096, dtype=torch.bfloat16)
+    gamma = randn(g, 4096)
+    y, m, rs = f.layer_norm(x, gamma, None)
+    want = f.layer_norm_backward(dy, x, gamma, m, rs)
+    got = _graphed(lambda: f.layer_norm_backward(dy, x, gamma, *f.layer_norm(x, gamma, None)[1:]))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_offsets_beyond_32_bits():
+    """Matrices of more than 4 GB: their last rows against the formulas."""
+    f = feat()
+    g = rng(31)
+    bf = torch.bfloat16
+    # 1,300,000 pairs of 2048: 5.3 GB on the pairs' side
+    T, K, D, E = 162500, 8, 2048, 16
+    ids = torch.randint(0, E, (T, K), generator=g, device="cuda").int()
+    x = torch.randn((T, D), generator=g, device="cuda", dtype=bf)
+    r = f.Route(T, K, E).build(ids)
+    xs = r.dispatch(x)
+    at = torch.cat([torch.arange(50, device="cuda"), torch.arange(T * K - 50, T * K, device="cuda")])
+    assert torch.equal(xs[at], x[r.order[at].long() // K])
+    back = r.combine(xs)
+    t = torch.arange(T - 40, T, device="cuda")
+    # eight equal rows: sums of a bfloat16 with itself
+    close(back[t], 8.0 * x[t].double(), 8 * U * 8 * x[t].double().abs())
+    del xs, back, x, r, ids
+    torch.cuda.empty_cache()
+    # 20,000 rows of 131,072 classes: 5.2 GB
+    T, V, M = 20000, 131072, 4
+    z = torch.randn((T, V), generator=g, device="cuda", dtype=bf)
+    tid, tl = torch.randint(0, V, (T, M), generator=g, device="cuda").int(), randn(g, T, M)
+    z1, rw = z[-3:].clone(), torch.ones(3, device="cuda")
+    loss, dz = f.distill(z, tid, tl, dlogits=z)
+    check_distill(z1, tid[-3:], tl[-3:], 1.0, rw, M, V, loss[-3:], dz[-3:])
+    del z, dz
+    torch.cuda.empty_cache()
+    # 700,000 rows of 4096: 5.7 GB
+    R, D = 700000, 4096
+    x = torch.randn((R, D), generator=g, device="cuda", dtype=bf)
+    x1 = x[-5:].clone()
+    y, m, rs = f.layer_norm(x, out=x)
+    want, m1, rs1 = f.layer_norm(x1)
+    # five rows alone may be shared out over other lanes: one rounding apart
+    assert float((y[-5:].double() - want.double()).abs().max()) <= 2.0 ** -8 * 2 * float(want.double().abs().max())
+    assert float((m[-5:] - m1).abs().max()) <= (D / 32 + 20) * U * float(x1.float().abs().mean(1).max()) * 2
+
+
+def test_many_experts_few_rows():
+    """More experts than pairs, a key of 24 bits."""
+    f = feat()
+    E = (1 << 23) + 5
+    ids = torch.tensor([[E - 1, 3], [-1, E], [3, 1 << 22]], dtype=torch.int32, device="cuda")
+    r = f.Route(3, 2, E).build(ids)
+    assert r.order.tolist() == [1, 4, 5, 0, -1, -1] and r.place.tolist() == [[3, 0], [-1, -1], [1, 2]]
+    assert r.offsets[[0, 3, 4, 1 << 22, (1 << 22) + 1, E - 1, E]].tolist() == [0, 0, 2, 2, 3, 3, 4]
