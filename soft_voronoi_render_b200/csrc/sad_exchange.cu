@@ -292,15 +292,19 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
 // ... of the group: 32 pairs a step, their rows by 32 / L groups side by side.
 // The ids of the pairs two steps ahead and the weights of the next are loaded
 // while the rows of a step are on their way.
-template <typename T, int VEC>
+template <typename T, int VEC, int NP>
 __device__ __forceinline__ void sum_run(const T *__restrict__ G, uint32_t ldg, const float *__restrict__ w,
                                         const int32_t *__restrict__ order, uint32_t n, uint32_t K, uint32_t a,
-                                        uint32_t b, int c, bool col, int log_l, float (&acc)[VEC + 1]) {
+                                        uint32_t b, int c, int D, int log_l, float (&acc)[NP][VEC + 1]) {
     const int L = 1 << log_l, S = 32 >> log_l;
     const int lane = threadIdx.x & 31, sub = lane >> log_l;
-    Two acc2[(VEC + 1) / 2];
+    const int step = VEC << log_l;
+    Two acc2[NP][(VEC + 1) / 2];
 #pragma unroll
-    for (int i = 0; i < (VEC + 1) / 2; ++i) acc2[i] = two(0.0f, 0.0f);
+    for (int v = 0; v < NP; ++v) {
+#pragma unroll
+        for (int i = 0; i < (VEC + 1) / 2; ++i) acc2[v][i] = two(0.0f, 0.0f);
+    }
     auto pair_at = [&](uint32_t s) { return s + lane < b ? (uint32_t)__ldg(order + s + lane) : 0xffffffffu; };
     auto weight_of = [&](uint32_t j) { return j < n ? __ldg(w + j) : 0.0f; };
     uint32_t j = pair_at(a), j_next = pair_at(a + 32);
@@ -311,31 +315,45 @@ __device__ __forceinline__ void sum_run(const T *__restrict__ G, uint32_t ldg, c
         const uint32_t j_ahead = pair_at(s + 64);
         float w_next = 0.0f;
         for (uint32_t q = 0; q < left; q += 4 * S) {
-            Pack<T, VEC> p[4];
+            Pack<T, VEC> p[4][NP];
             float wq[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const uint32_t at = q + u * S + sub;
                 const uint32_t r = __shfl_sync(0xffffffffu, row, at & 31);
                 wq[u] = __shfl_sync(0xffffffffu, wj, at & 31);
-                p[u].clear();
-                if (at < left && col) p[u] = load_pack<T, VEC>(at_row(G, r, ldg, c));
+                const T *from = at_row(G, r, ldg, c);
+#pragma unroll
+                for (int v = 0; v < NP; ++v) {
+                    p[u][v].clear();
+                    if (at < left && c + v * step < D) p[u][v] = load_pack<T, VEC>(from + v * step);
+                }
             }
             if (q == 0) w_next = weight_of(j_next);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) add_scaled(p[u], wq[u], acc2);  // 0 beyond the run
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int v = 0; v < NP; ++v) add_scaled(p[u][v], wq[u], acc2[v]);  // 0 beyond the run
+            }
         }
         j = j_next;
         wj = w_next;
         j_next = j_ahead;
     }
 #pragma unroll
-    for (int i = 0; i < VEC; i += 2) both(acc2[i / 2], acc[i], acc[i + 1]);
-    for (int o = L; o < 32; o <<= 1) {
+    for (int v = 0; v < NP; ++v) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        for (int i = 0; i < VEC; i += 2) both(acc2[v][i / 2], acc[v][i], acc[v][i + 1]);
+        for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[v][i] += __shfl_xor_sync(0xffffffffu, acc[v][i], o);
+        }
     }
 }
+
+// pieces a lane: one of 16 bytes, or four smaller ones (a row of 41 elements
+// on 32 lanes left most of them idle in its second part)
+template <typename T, int VEC> constexpr int lane_pieces() { return VEC * sizeof(T) == 16 ? 1 : 4; }
 
 // to[i] = acc[i], by the first group; `to` may start anywhere on 4 bytes
 template <int VEC> __device__ __forceinline__ void store_sums(float *to, const float (&acc)[VEC + 1]) {
@@ -379,9 +397,10 @@ __global__ void __launch_bounds__(THREADS, 4) chunk_kernel(const T *__restrict__
     if (lo >= total) return;
     const uint32_t hi = min(lo + C, total);
     const int first = expert_at(offsets, E, lo);
-    for (int slab = blockIdx.y * 32 * VEC; slab < D; slab += gridDim.y * 32 * VEC) {
+    constexpr int NP = lane_pieces<T, VEC>();
+    const int step = VEC << log_l, wide = NP * step;
+    for (int slab = blockIdx.y * wide; slab < D; slab += gridDim.y * wide) {
         const int c = slab + in_row * VEC;
-        const bool col = c < D;
         int e = first;
         uint32_t a = lo;
         while (a < hi && e < E) {
@@ -391,16 +410,16 @@ __global__ void __launch_bounds__(THREADS, 4) chunk_kernel(const T *__restrict__
                 continue;
             }
             const uint32_t b = min(end, hi);
-            float acc[VEC + 1];
-            sum_run<T, VEC>(G, ldg, w, order, n, (uint32_t)K, a, b, c, col, log_l, acc);
+            float acc[NP][VEC + 1];
+            sum_run<T, VEC, NP>(G, ldg, w, order, n, (uint32_t)K, a, b, c, D, log_l, acc);
             const uint32_t from = (uint32_t)__ldg(offsets + e);
             const bool whole = from == a && end == b;
             // the expert that starts in this chunk and goes on behind it
             if (lane == 0 && slab == 0 && from >= lo && end > b) cut_expert[chunk] = e;
-            if (lane >> log_l == 0 && col)
-                store_sums<VEC>(whole ? dF + (long long)e * D + c
-                                      : partial + ((size_t)2 * chunk + (a == lo ? 0 : 1)) * D + c,
-                                acc);
+            float *to = whole ? dF + (long long)e * D : partial + ((size_t)2 * chunk + (a == lo ? 0 : 1)) * D;
+#pragma unroll
+            for (int v = 0; v < NP; ++v)
+                if (lane >> log_l == 0 && c + v * step < D) store_sums<VEC>(to + c + v * step, acc[v]);
             a = b;
             ++e;
         }
@@ -563,12 +582,16 @@ __global__ void __launch_bounds__(THREADS, 4) piece_kernel(const T *__restrict__
     if (piece.y >= pieces_of(from, end, C)) return;
     const uint32_t a = from + piece.y * C, b = min(a + C, end);
     const bool whole = end - from <= C;
-    for (int slab = blockIdx.y * 32 * VEC; slab < D; slab += gridDim.y * 32 * VEC) {
+    constexpr int NP = lane_pieces<T, VEC>();
+    const int step = VEC << log_l, wide = NP * step;
+    for (int slab = blockIdx.y * wide; slab < D; slab += gridDim.y * wide) {
         const int c = slab + in_row * VEC;
-        float acc[VEC + 1];
-        sum_run<T, VEC>(G, ldg, w, order, n, (uint32_t)K, a, b, c, c < D, log_l, acc);
-        if (lane >> log_l == 0 && c < D)
-            store_sums<VEC>(whole ? dF + (long long)piece.x * D + c : partial + piece_row(from, piece.y, C) * D + c, acc);
+        float acc[NP][VEC + 1];
+        sum_run<T, VEC, NP>(G, ldg, w, order, n, (uint32_t)K, a, b, c, D, log_l, acc);
+        float *to = whole ? dF + (long long)piece.x * D : partial + piece_row(from, piece.y, C) * D;
+#pragma unroll
+        for (int v = 0; v < NP; ++v)
+            if (lane >> log_l == 0 && c + v * step < D) store_sums<VEC>(to + c + v * step, acc[v]);
     }
 }
 
@@ -620,12 +643,21 @@ struct Shape {
     bool row_per_block;
 };
 
-// A row's pieces beyond a warp's 32 are looped over by that warp, unless the
-// rows are too few to give every SM eight warps: then a block shares a row.
-Shape shape_of(long long n, int D, int vec) {
+// A group loops over its row's pieces.  With fewer lanes a row's ids, weights
+// and dot products are handled fewer times over, with more the loads of a row
+// lie closer: 16-byte pieces, two a lane (2048 x 2048 x 32 bf16: blend 190 us
+// with two lanes, 212 with four; 768 x 512 x 64 f16: 38 with four, 43 with
+// eight, 53 with two); smaller ones, up to eight a lane while a group's load
+// has 16 bytes (768 x 512 x 41 f32: 74 to 86 us, 168 with 32 lanes).  Few rows
+// get all the lanes that a row has pieces for, and wide ones a block.
+Shape shape_of(long long n, int D, int vec, int bytes) {
     Shape s;
     s.log_l = group_log(D, vec);
     s.row_per_block = D > 32 * vec && n < 148 * 8;
+    const int pieces = (D + vec - 1) / vec;
+    const int fewest = vec * bytes == 16 ? max(1, s.log_l - 1)
+                                         : min(5, max(ceil_log2(16 / (vec * bytes)), ceil_log2((pieces + 7) / 8)));
+    while (!s.row_per_block && pieces <= 256 && s.log_l > fewest && (n << (s.log_l - 1)) / 32 >= 148 * 64) --s.log_l;
     const long long per_block = s.row_per_block ? 1 : THREADS >> s.log_l;
     s.blocks = (unsigned)((n + per_block - 1) / per_block);
     return s;
@@ -651,7 +683,7 @@ cudaError_t gather(RowsIn rows, const int32_t *at, long long n_at, const float *
                    int D, RowsOut out, float *dots, cudaStream_t st) {
     const T *r = static_cast<const T *>(rows.p), *g = static_cast<const T *>(other.p);
     T *o = static_cast<T *>(out.p);
-    const Shape s = shape_of(n, D, VEC);
+    const Shape s = shape_of(n, D, VEC, sizeof(T));
     const uint32_t m = (uint32_t)n_at;
     const bool full = K == K_MAX && aligned16(at) && aligned16(w) && aligned16(dots);
     if (o && dots) {
@@ -685,7 +717,7 @@ cudaError_t spread(RowsIn x, const int32_t *at, long long n_at, const float *w, 
                    int D, RowsOut to, float *dots, cudaStream_t st) {
     const T *xp = static_cast<const T *>(x.p), *r = static_cast<const T *>(rows.p);
     T *o = static_cast<T *>(to.p);
-    const Shape s = shape_of(n, D, VEC);
+    const Shape s = shape_of(n, D, VEC, sizeof(T));
     const uint32_t m = (uint32_t)n_at;
     const bool full = K == K_MAX && aligned16(at) && aligned16(w) && aligned16(dots);
     if (dots) {
@@ -773,12 +805,14 @@ cudaError_t segments(RowsIn g, const float *w, const int32_t *offsets, const int
     const bool far = is_far(n / K, D, sizeof(T));
     const Space s(ws, n, E, D, far);
     const T *G = static_cast<const T *>(g.p);
-    const unsigned slabs = (unsigned)min((D + 32 * VEC - 1) / (32 * VEC), 65535);
+    constexpr int NP = lane_pieces<T, VEC>();
+    const int log_l = group_log(D, NP * VEC), wide = (NP * VEC) << log_l;
+    const unsigned slabs = (unsigned)min((D + wide - 1) / wide, 65535);
     const uint32_t m = (uint32_t)n;
     if (!far) {
         const dim3 grid((s.chunks + WARPS - 1) / WARPS, slabs);
         chunk_kernel<T, VEC><<<grid, THREADS, 0, st>>>(G, row_bytes<T>(g.ld), w, offsets, order, m, K, E, D,
-                                                       group_log(D, VEC), s.C, s.chunks, dF, s.partial, s.cut_expert);
+                                                       log_l, s.C, s.chunks, dF, s.partial, s.cut_expert);
         if (s.chunks > 1)
             join_kernel<<<(s.chunks + WARPS - 1) / WARPS, THREADS, 0, st>>>(offsets, s.cut_expert, m, E, D, s.C,
                                                                             s.chunks, s.partial, dF);
@@ -793,7 +827,7 @@ cudaError_t segments(RowsIn g, const float *w, const int32_t *offsets, const int
     turn_kernel<true><<<experts, THREADS, 0, st>>>(offsets, order, m, E, per, s.C, s.count, s.most, s.turn);
     const dim3 grid((s.most + WARPS - 1) / WARPS, slabs);
     piece_kernel<T, VEC><<<grid, THREADS, 0, st>>>(G, row_bytes<T>(g.ld), w, offsets, order, m, K, E, D,
-                                                   group_log(D, VEC), s.C, s.count, s.most, s.turn, dF, s.partial);
+                                                   log_l, s.C, s.count, s.most, s.turn, dF, s.partial);
     piece_join_kernel<<<experts, THREADS, 0, st>>>(offsets, m, E, per, D, s.C, s.partial, dF);
     return cudaGetLastError();
 }
