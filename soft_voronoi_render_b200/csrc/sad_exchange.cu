@@ -299,6 +299,7 @@ __device__ __forceinline__ void sum_run(const T *__restrict__ G, uint32_t ldg, c
     const int L = 1 << log_l, S = 32 >> log_l;
     const int lane = threadIdx.x & 31, sub = lane >> log_l;
     const int step = VEC << log_l;
+    constexpr int U = NP == 1 ? 4 : 2;  // rows of a group on their way
     Two acc2[NP][(VEC + 1) / 2];
 #pragma unroll
     for (int v = 0; v < NP; ++v) {
@@ -314,11 +315,11 @@ __device__ __forceinline__ void sum_run(const T *__restrict__ G, uint32_t ldg, c
         const uint32_t left = min(b - s, 32u);
         const uint32_t j_ahead = pair_at(s + 64);
         float w_next = 0.0f;
-        for (uint32_t q = 0; q < left; q += 4 * S) {
-            Pack<T, VEC> p[4][NP];
-            float wq[4];
+        for (uint32_t q = 0; q < left; q += U * S) {
+            Pack<T, VEC> p[U][NP];
+            float wq[U];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const uint32_t at = q + u * S + sub;
                 const uint32_t r = __shfl_sync(0xffffffffu, row, at & 31);
                 wq[u] = __shfl_sync(0xffffffffu, wj, at & 31);
@@ -331,7 +332,7 @@ __device__ __forceinline__ void sum_run(const T *__restrict__ G, uint32_t ldg, c
             }
             if (q == 0) w_next = weight_of(j_next);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int v = 0; v < NP; ++v) add_scaled(p[u][v], wq[u], acc2[v]);  // 0 beyond the run
             }
@@ -351,9 +352,9 @@ __device__ __forceinline__ void sum_run(const T *__restrict__ G, uint32_t ldg, c
     }
 }
 
-// pieces a lane: one of 16 bytes, or four smaller ones (a row of 41 elements
+// pieces a lane: one of 16 bytes, or eight smaller ones (a row of 41 elements
 // on 32 lanes left most of them idle in its second part)
-template <typename T, int VEC> constexpr int lane_pieces() { return VEC * sizeof(T) == 16 ? 1 : 4; }
+template <typename T, int VEC> constexpr int lane_pieces() { return VEC * sizeof(T) == 16 ? 1 : 8; }
 
 // to[i] = acc[i], by the first group; `to` may start anywhere on 4 bytes
 template <int VEC> __device__ __forceinline__ void store_sums(float *to, const float (&acc)[VEC + 1]) {
