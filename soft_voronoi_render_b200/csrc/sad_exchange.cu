@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(THREADS) spread_kernel(const T *__restrict__ X
 // ---------------------------------------------------------------------------
 // segment sums
 //
-// Near rows (dout within half of the L2): the sorted pairs are cut into chunks
+// Near rows (is_far says which): the sorted pairs are cut into chunks
 // of C positions, a warp each, whatever the experts' shares are.  A warp walks
 // its chunk's runs of one expert; a run that is all of its expert's pairs goes
 // to dF, one that is cut at the chunk's start or end to one of the chunk's two
@@ -766,9 +766,15 @@ uint32_t chunk_of(long long n, int E, bool far) {
     return (uint32_t)c;
 }
 
-// dout beyond half of the L2
+// Far rows: dout beyond half of the L2; and from 2^21 pairs on pieces pay for
+// their three small kernels anyway, since whole experts leave no partial rows
+// (768 x 512 x 64 f16, 50,000 sites: 141 us against 164 by chunks; 512 x 256,
+// 2,000 sites: 100 against 57).
 constexpr size_t FAR_BYTES = 64u << 20;
-bool is_far(long long n_rows, int D, size_t element) { return (size_t)n_rows * D * element > FAR_BYTES; }
+constexpr long long FAR_PAIRS = 1 << 21;
+bool is_far(long long n_rows, int K, int D, size_t element) {
+    return n_rows * K >= FAR_PAIRS || (size_t)n_rows * D * element > FAR_BYTES;
+}
 
 size_t up(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -803,7 +809,7 @@ struct Space {
 template <typename T, int VEC>
 cudaError_t segments(RowsIn g, const float *w, const int32_t *offsets, const int32_t *order, long long n, int K,
                      int E, int D, float *dF, void *ws, cudaStream_t st) {
-    const bool far = is_far(n / K, D, sizeof(T));
+    const bool far = is_far(n / K, K, D, sizeof(T));
     const Space s(ws, n, E, D, far);
     const T *G = static_cast<const T *>(g.p);
     constexpr int NP = lane_pieces<T, VEC>();
@@ -858,7 +864,7 @@ cudaError_t launch_spread(int dtype, RowsIn x, const int32_t *at, long long n_at
 size_t segment_workspace_bytes(long long n_rows, int K, int E, int D) {
     // of any element type: whether rows are far depends on it
     const long long n = n_rows * K;
-    return max(Space(nullptr, n, E, D, false).bytes, is_far(n_rows, D, 4) ? Space(nullptr, n, E, D, true).bytes : 0);
+    return max(Space(nullptr, n, E, D, false).bytes, is_far(n_rows, K, D, 4) ? Space(nullptr, n, E, D, true).bytes : 0);
 }
 
 cudaError_t launch_segment_sums(int dtype, RowsIn dout, const float *w, const int32_t *offsets, const int32_t *order,
