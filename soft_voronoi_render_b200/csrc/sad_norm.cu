@@ -62,6 +62,13 @@ template <typename T, int VEC, int NV> struct RowPart {
     }
 };
 
+// s / D with inv = 1 / D: the quotient's remainder corrects it, so that a row of
+// equal elements has exactly that mean
+__device__ __forceinline__ float mean_of(float s, float D, float inv) {
+    const float m = s * inv;
+    return fmaf(fmaf(-m, D, s), inv, m);
+}
+
 // the most threads of a block that shares a row of at most 16384 elements
 constexpr int block_bound(int vec, int nv) { return 16384 / vec / nv < 1024 ? 16384 / vec / nv : 1024; }
 
@@ -114,7 +121,8 @@ __global__ void __launch_bounds__(BLOCK ? block_bound(VEC, NV) : THREADS) norm_k
 #pragma unroll
         for (int q = 0; q < VEC; ++q) s += row.p[i].get(q);
     }
-    const float m = (BLOCK ? block_sum(s, scratch[0]) : lanes_sum(s, L)) / (float)D;
+    const float inv = 1.0f / (float)D;
+    const float m = mean_of(BLOCK ? block_sum(s, scratch[0]) : lanes_sum(s, L), (float)D, inv);
     row.stay_packed();
     s = 0.0f;
 #pragma unroll
@@ -127,7 +135,8 @@ __global__ void __launch_bounds__(BLOCK ? block_bound(VEC, NV) : THREADS) norm_k
             }
         }
     }
-    const float rs = 1.0f / sqrtf((BLOCK ? block_sum(s, scratch[1]) : lanes_sum(s, L)) / (float)D + eps);
+    // rsqrtf is within 2 ulp
+    const float rs = rsqrtf(fmaf(BLOCK ? block_sum(s, scratch[1]) : lanes_sum(s, L), inv, eps));
     if (!in) return;
     row.stay_packed();
 #pragma unroll
@@ -377,6 +386,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, 
     const long long r0 = (long long)blockIdx.x * ROWS;
     const int c0 = threadIdx.x * VEC, step = blockDim.x * VEC;
     RowPart<T, VEC, NV> row[ROWS];
+    const float inv = 1.0f / (float)D;
     float s[ROWS], m[ROWS], rs[ROWS];
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) row[j].load(x + (r0 + j) * ldx, c0, step, r0 + j < n ? D : 0);
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, 
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
         row[j].stay_packed();
-        m[j] /= (float)D;
+        m[j] = mean_of(m[j], (float)D, inv);
         Two sum = two(0.0f, 0.0f);
         const Two mm = two(-m[j], -m[j]);
 #pragma unroll
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const T *x, 
 #pragma unroll
     for (int j = 0; j < ROWS; ++j) {
         row[j].stay_packed();
-        rs[j] = 1.0f / sqrtf(rs[j] / (float)D + eps);
+        rs[j] = rsqrtf(fmaf(rs[j], inv, eps));
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -733,7 +743,9 @@ cudaError_t forward(RowsIn x, const float *gamma, const float *beta, float eps, 
     }
     // fewer rows than four a multiprocessor: as many lanes a row as there are
     const bool few = n < SMS * 4 && pieces > 64;
-    const int most = few ? (pieces <= 2048 ? 2 : pieces <= 8192 ? 8 : 16) : pieces <= 64 ? 2 : pieces <= 256 ? 8 : 16;
+    // otherwise few lanes: what a row costs beside its elements (430
+    // instructions a warp) is shared by the rows of a warp
+    const int most = few ? (pieces <= 2048 ? 2 : pieces <= 8192 ? 8 : 16) : pieces <= 128 ? 8 : 16;
     const Shape s = shape_of(n, pieces, most, few || pieces > 512);
     if (most == 2) forward_shape<T, VEC, 2>(s, x, gamma, beta, eps, n, D, y, mean, rstd, st);
     else if (most == 8) forward_shape<T, VEC, 8>(s, x, gamma, beta, eps, n, D, y, mean, rstd, st);
