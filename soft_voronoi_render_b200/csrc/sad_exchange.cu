@@ -167,7 +167,7 @@ __device__ __forceinline__ void finish_dots(float (&dot)[K_MAX], int L, int lane
 // Empty slots are rows of zeros with weight 0, so that nothing branches
 // between the rows but the loads themselves.
 template <typename T, int VEC, bool FULL, bool SUM, bool DOT, bool ROW_PER_BLOCK>
-__global__ void __launch_bounds__(THREADS, SUM && DOT ? 3 : 4) gather_kernel(const T *__restrict__ R, uint32_t ldr,
+__global__ void __launch_bounds__(THREADS, SUM && DOT ? 3 : SUM ? 4 : 5) gather_kernel(const T *__restrict__ R, uint32_t ldr,
                                                             const int32_t *__restrict__ at, uint32_t n_at,
                                                             const float *__restrict__ w, const T *__restrict__ G,
                                                             uint32_t ldg, long long n_rows, int K, int D, int log_l,
