@@ -549,7 +549,8 @@ int sad_blend_weights(sad_ctx *ctx, int32_t *ids, float *weights, sad_stream_t s
  * = number of pairs whose id is valid and below e; place int32 [T][K] = the
  * pair's position, offsets[e] + (earlier pairs of the same e), or -1 for an
  * empty slot; order int32 [n] with order[place[j]] = j, and -1 behind the
- * last pair.  1 <= n_sites < 2^30. */
+ * last pair.  1 <= n_sites < 2^30.  The workspace grows with n: up to 28 bytes
+ * a pair. */
 int sad_route_workspace_bytes(int64_t n_rows, int K, int n_sites, size_t *bytes);
 int sad_route(const int32_t *ids, int64_t n_rows, int K, int n_sites, int32_t *offsets, int32_t *order,
               int32_t *place, void *workspace, size_t workspace_bytes, sad_stream_t stream);

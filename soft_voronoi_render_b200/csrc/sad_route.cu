@@ -20,8 +20,9 @@
 //
 // Measured: those lists 462 us (0.13 of the copy rate by the floor's bytes; 196
 // us of it the tiles' sort, bound by instructions and shared memory, 107 us
-// their writing, 100 us the runs' sort); 65,536 x 8 pairs of 512 experts 22 us,
-// up to 1024 pairs 3 us in one launch.
+// their writing, 100 us the runs' sort); 768 x 512 x 8 pairs of
+// 50,000 sites 95 us, 65,536 x 8 of 512 experts 27 us, up to 1024 pairs 3 us in
+// one launch.
 #include "sad_features.h"
 
 namespace sad {
@@ -42,11 +43,14 @@ struct Plan {
     bool by_runs;
 };
 
-// tiles that are sorted in shared memory, and the pairs from which on they
-// are: below, their dozen launches cost more than the scattered writes
+// Tiles that are sorted in shared memory, and the pairs from which on they are:
+// a dozen launches against the scattered writes of seven.  Lists of images:
+// 393,216 x 8 122 us by runs, 95 without; 1,048,576 x 8 206 and 233; 4,194,304
+// x 8 462 and 1,040.  (Random lists of 4,194,304 x 8 over 131,072 sites have no
+// runs: 3.6 ms against 2.4.)
 constexpr int RUN_ITEMS = 16;
 constexpr int RUN_TILE = THREADS * RUN_ITEMS;
-constexpr long long RUN_PAIRS = 1 << 20;
+constexpr long long RUN_PAIRS = 3 << 21;
 constexpr int TILE_BITS = 12;      // a place in a tile, or a run's length less 1 ...
 constexpr int RUN_KEY_BITS = 20;   // ... in one word with the key
 static_assert(RUN_TILE == 1 << TILE_BITS && TILE_BITS + RUN_KEY_BITS == 32, "one word a pair");

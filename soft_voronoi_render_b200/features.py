@@ -90,9 +90,10 @@ class Route:
 
     ``build`` fills ``offsets`` (n_sites + 1), ``order`` (n_rows * K) and
     ``place`` (n_rows, K) for the ids it is given, in stream order; the calls
-    after it go by those until the next build.  A Route owns one workspace:
-    builds of one Route must not overlap on the GPU (use one Route per
-    stream, and one per captured graph that may run beside another).
+    after it go by those until the next build.  A Route owns one workspace (up
+    to 28 bytes a pair): builds of one Route must not overlap on the GPU (use
+    one Route per stream, and one per captured graph that may run beside
+    another).
     """
 
     def __init__(self, n_rows: int, K: int, n_sites: int, device="cuda"):

@@ -679,10 +679,11 @@ def test_blend_backward_beyond_the_cache(T, E, D, dt):
 
 
 @pytest.mark.parametrize("kind", ["random", "coherent", "one", "none", "sorted", "reversed", "two"])
-@pytest.mark.parametrize("T,K,E", [(131072, 8, 1024), (131073, 8, 5000), (150001, 7, 131072), (1048577, 1, 1 << 20),
-                                   (140000, 8, 1 << 21), (262144, 4, 60000)])
+@pytest.mark.parametrize("T,K,E", [(786432, 8, 1024), (786433, 8, 5000), (900001, 7, 131072),
+                                   (6300001, 1, (1 << 20) - 1), (131073, 8, 5000), (1048577, 1, 1 << 20),
+                                   (790000, 8, 1 << 21), (1600000, 4, 60000)])
 def test_route_of_many_pairs(T, K, E, kind):
-    """From 2^20 pairs and 1024 sites on the tiles' runs are sorted: the same
+    """From 3 * 2^21 pairs and 1024 sites on the tiles' runs are sorted: the same
     whole numbers, whatever the runs are."""
     g = rng(T + E)
     j = torch.arange(T * K, device="cuda")
@@ -734,7 +735,7 @@ def test_captured_large_forms():
     want = f.distill(z, tid, tl)
     got = _graphed(lambda: f.distill(z, tid, tl))
     assert all(torch.equal(a, b) for a, b in zip(want, got))
-    T, E, D = 300000, 5000, 64
+    T, E, D = 800000, 5000, 24
     ids = ((torch.arange(T * 8, device="cuda") // 50 * 77 + torch.randint(0, 5, (T * 8,), generator=g, device="cuda"))
            % E).int().view(T, 8).contiguous()
     w = torch.rand((T, 8), generator=g, device="cuda")
