@@ -89,7 +89,7 @@ __device__ __forceinline__ void list_length(const uint32_t *__restrict__ length,
 
 // counts[digit][block]
 __global__ void __launch_bounds__(THREADS) count_kernel(const int32_t *__restrict__ ids,
-                                                        const uint32_t *__restrict__ keys, long long n, int E,
+                                                        const uint2 *__restrict__ items, long long n, int E,
                                                         long long per_block, int shift, int bits,
                                                         uint32_t *__restrict__ counts,
                                                         const uint32_t *__restrict__ length) {
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(THREADS) count_kernel(const int32_t *__restric
     __syncthreads();
     const long long lo = blockIdx.x * per_block, hi = min(n, lo + per_block);
     for (long long i = lo + threadIdx.x; i < hi; i += THREADS) {
-        const uint32_t k = keys ? keys[i] : key_of(ids[i], E);
+        const uint32_t k = items ? items[i].x : key_of(ids[i], E);
         atomicAdd(&hist[k >> shift & (D - 1)], 1u);
     }
     __syncthreads();
@@ -162,16 +162,14 @@ __device__ void digit_bases(const uint32_t *__restrict__ totals, int D, uint32_t
     }
 }
 
-// moves every item to its digit's place.  The first pass reads ids (the pair
-// is the index); the last writes order and place instead of keys and pairs.
+// moves every item, a key and its pair, to its digit's place.  The first pass
+// reads ids (the pair is the index); the last writes order and place.
 __global__ void __launch_bounds__(THREADS, 4) move_kernel(const int32_t *__restrict__ ids,
-                                                       const uint32_t *__restrict__ keys,
-                                                       const uint32_t *__restrict__ pairs, long long n, int E,
+                                                       const uint2 *__restrict__ items, long long n, int E,
                                                        long long per_block, int shift, int bits,
                                                        const uint32_t *__restrict__ counts,
                                                        const uint32_t *__restrict__ totals,
-                                                       uint32_t *__restrict__ keys_out,
-                                                       uint32_t *__restrict__ pairs_out,
+                                                       uint2 *__restrict__ items_out,
                                                        int32_t *__restrict__ order, int32_t *__restrict__ place,
                                                        int32_t *__restrict__ offsets,
                                                        const uint32_t *__restrict__ length) {
@@ -198,8 +196,10 @@ __global__ void __launch_bounds__(THREADS, 4) move_kernel(const int32_t *__restr
         for (int q = 0; q < ITEMS; ++q) {
             const long long i = t0 + warp * (32 * ITEMS) + q * 32 + lane;
             const bool in = i < hi;
-            key[q] = in ? (keys ? keys[i] : key_of(ids[i], E)) : 0xffffffffu;
-            pair[q] = in ? (pairs ? pairs[i] : (uint32_t)i) : 0;
+            uint2 v = make_uint2(0xffffffffu, 0);
+            if (in) v = items ? items[i] : make_uint2(key_of(ids[i], E), (uint32_t)i);
+            key[q] = v.x;
+            pair[q] = v.y;
         }
 #pragma unroll
         for (int q = 0; q < ITEMS; ++q) {
@@ -243,8 +243,7 @@ __global__ void __launch_bounds__(THREADS, 4) move_kernel(const int32_t *__restr
                 order[pos] = empty ? -1 : (int32_t)pair[q];
                 place[pair[q]] = empty ? -1 : (int32_t)pos;
             } else {
-                keys_out[pos] = key[q];
-                pairs_out[pos] = pair[q];
+                items_out[pos] = make_uint2(key[q], pair[q]);
             }
         }
         __syncthreads();
@@ -465,13 +464,10 @@ __global__ void __launch_bounds__(1024) run_base_kernel(const uint32_t *__restri
 // the runs of all tiles behind one another: word, and the run's entry
 __global__ void __launch_bounds__(THREADS) run_list_kernel(const uint32_t *__restrict__ run_word,
                                                            const uint32_t *__restrict__ base,
-                                                           uint32_t *__restrict__ word, uint32_t *__restrict__ entry) {
+                                                           uint2 *__restrict__ items) {
     const uint32_t from = base[blockIdx.x], count = base[blockIdx.x + 1] - from;
     const uint32_t t0 = blockIdx.x * (uint32_t)RUN_TILE;
-    for (uint32_t r = threadIdx.x; r < count; r += THREADS) {
-        word[from + r] = run_word[t0 + r];
-        entry[from + r] = t0 + r;
-    }
+    for (uint32_t r = threadIdx.x; r < count; r += THREADS) items[from + r] = make_uint2(run_word[t0 + r], t0 + r);
 }
 
 // pairs of a run, from its word
@@ -480,14 +476,14 @@ __device__ __forceinline__ uint32_t run_length(uint32_t word) { return (word & (
 // The sorted runs' first positions: a run of runs a block, its sum first,
 // then its scan behind the sums of the blocks before it.  where[entry] is the
 // position for the tiles, sorted[i] the same by rank for the offsets.
-__global__ void __launch_bounds__(THREADS) run_sum_kernel(const uint32_t *__restrict__ word,
+__global__ void __launch_bounds__(THREADS) run_sum_kernel(const uint2 *__restrict__ items,
                                                           const uint32_t *__restrict__ length,
                                                           uint32_t *__restrict__ sums) {
     __shared__ uint32_t warp_sum[WARPS];
     const uint32_t total = *length, each = (total + gridDim.x - 1) / gridDim.x;
     const uint32_t lo = min(blockIdx.x * each, total), hi = min(lo + each, total);
     uint32_t s = 0;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += THREADS) s += run_length(word[i]);
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += THREADS) s += run_length(items[i].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
@@ -498,8 +494,7 @@ __global__ void __launch_bounds__(THREADS) run_sum_kernel(const uint32_t *__rest
         sums[blockIdx.x] = s;
     }
 }
-__global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__restrict__ word,
-                                                            const uint32_t *__restrict__ entry,
+__global__ void __launch_bounds__(THREADS) run_place_kernel(const uint2 *__restrict__ items,
                                                             const uint32_t *__restrict__ length,
                                                             const uint32_t *__restrict__ sums,
                                                             uint32_t *__restrict__ where,
@@ -519,7 +514,8 @@ __global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__re
     __syncthreads();
     for (uint32_t i0 = lo; i0 < hi; i0 += THREADS) {
         const uint32_t i = i0 + threadIdx.x;
-        const uint32_t e = i < hi ? entry[i] : 0, v = i < hi ? run_length(word[i]) : 0;
+        const uint2 run = i < hi ? items[i] : make_uint2(0, 0);
+        const uint32_t e = run.y, v = i < hi ? run_length(run.x) : 0;
         uint32_t s = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -543,7 +539,7 @@ __global__ void __launch_bounds__(THREADS) run_place_kernel(const uint32_t *__re
 }
 
 // offsets[e]: the first position of the first run with a key of e or more
-__global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__restrict__ word,
+__global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint2 *__restrict__ items,
                                                               const uint32_t *__restrict__ sorted,
                                                               const uint32_t *__restrict__ length, long long n, int E,
                                                               int32_t *__restrict__ offsets) {
@@ -553,7 +549,7 @@ __global__ void __launch_bounds__(THREADS) run_offsets_kernel(const uint32_t *__
     uint32_t lo = 0, hi = total;
     while (lo < hi) {
         const uint32_t mid = (lo + hi) >> 1;
-        if (__ldg(word + mid) >> TILE_BITS < (uint32_t)e) lo = mid + 1;
+        if (__ldg(&items[mid].x) >> TILE_BITS < (uint32_t)e) lo = mid + 1;
         else hi = mid;
     }
     offsets[e] = (int32_t)(lo < total ? sorted[lo] : (uint32_t)n);
@@ -618,7 +614,8 @@ __global__ void __launch_bounds__(THREADS, 6) tile_write_kernel(long long n, con
 
 // workspace of the sort by runs
 struct RunSpace {
-    uint32_t *totals, *counts, *base, *run_count, *heads, *sums, *run_word, *list[2][2];
+    uint32_t *totals, *counts, *base, *run_count, *heads, *sums, *run_word;
+    uint2 *list[2];  // runs: key and length, entry
     uint16_t *local, *run_start, *heads_before;
     int tiles;
     size_t bytes;
@@ -640,8 +637,7 @@ struct RunSpace {
         sums = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * RUN_BLOCKS));
         heads_before = reinterpret_cast<uint16_t *>(take(slots / 16));
         run_word = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * slots));
-        for (int g = 0; g < 2; ++g)
-            for (int h = 0; h < 2; ++h) list[g][h] = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t) * slots));
+        for (int g = 0; g < 2; ++g) list[g] = reinterpret_cast<uint2 *>(take(sizeof(uint2) * slots));
         local = reinterpret_cast<uint16_t *>(take(sizeof(uint16_t) * slots));
         run_start = reinterpret_cast<uint16_t *>(take(sizeof(uint16_t) * slots));
         bytes = at;
@@ -657,23 +653,24 @@ cudaError_t route_by_runs(const int32_t *ids, long long n, int E, const Plan &p,
     tile_sort_kernel<<<s.tiles, THREADS, sort_shared, st>>>(ids, n, E, p.passes, p.bits, s.local, s.heads,
                                                             s.heads_before, s.run_word, s.run_start, s.run_count);
     run_base_kernel<<<1, 1024, 0, st>>>(s.run_count, s.tiles, s.base);
-    run_list_kernel<<<s.tiles, THREADS, 0, st>>>(s.run_word, s.base, s.list[0][0], s.list[0][1]);
+    run_list_kernel<<<s.tiles, THREADS, 0, st>>>(s.run_word, s.base, s.list[0]);
     for (int q = 0; q < p.passes; ++q) {
-        uint32_t *const *from = s.list[q & 1], *const *to = s.list[~q & 1];
+        const uint2 *from = s.list[q & 1];
         const long long slots = (long long)s.tiles * RUN_TILE;
         const int shift = TILE_BITS + q * p.bits;
-        count_kernel<<<RUN_BLOCKS, THREADS, D * sizeof(uint32_t), st>>>(nullptr, from[0], slots, E, 0, shift, p.bits,
+        count_kernel<<<RUN_BLOCKS, THREADS, D * sizeof(uint32_t), st>>>(nullptr, from, slots, E, 0, shift, p.bits,
                                                                         s.counts, length);
         scan_kernel<<<D, THREADS, 0, st>>>(s.counts, RUN_BLOCKS, s.totals);
-        move_kernel<<<RUN_BLOCKS, THREADS, move_shared(D), st>>>(
-            nullptr, from[0], from[1], slots, E, 0, shift, p.bits, s.counts, s.totals, to[0], to[1], nullptr, nullptr,
-            nullptr, length);
+        move_kernel<<<RUN_BLOCKS, THREADS, move_shared(D), st>>>(nullptr, from, slots, E, 0, shift, p.bits, s.counts,
+                                                                 s.totals, s.list[~q & 1], nullptr, nullptr, nullptr,
+                                                                 length);
     }
-    uint32_t *const *sorted = s.list[p.passes & 1], *const *spare = s.list[~p.passes & 1];
-    // the words of the tiles' runs are in the lists: their place takes the positions
-    run_sum_kernel<<<RUN_BLOCKS, THREADS, 0, st>>>(sorted[0], length, s.sums);
-    run_place_kernel<<<RUN_BLOCKS, THREADS, 0, st>>>(sorted[0], sorted[1], length, s.sums, s.run_word, spare[0]);
-    run_offsets_kernel<<<E / THREADS + 1, THREADS, 0, st>>>(sorted[0], spare[0], length, n, E, offsets);
+    const uint2 *runs = s.list[p.passes & 1];
+    uint32_t *sorted = reinterpret_cast<uint32_t *>(s.list[~p.passes & 1]);
+    // the words of the tiles' runs are in the list: their place takes the positions
+    run_sum_kernel<<<RUN_BLOCKS, THREADS, 0, st>>>(runs, length, s.sums);
+    run_place_kernel<<<RUN_BLOCKS, THREADS, 0, st>>>(runs, length, s.sums, s.run_word, sorted);
+    run_offsets_kernel<<<E / THREADS + 1, THREADS, 0, st>>>(runs, sorted, length, n, E, offsets);
     tile_write_kernel<<<s.tiles, THREADS, 0, st>>>(n, s.local, s.heads, s.heads_before, s.run_word, s.run_start,
                                                    s.run_count, offsets, E, order, place);
     return cudaGetLastError();
@@ -733,8 +730,8 @@ size_t route_workspace_bytes(long long n_rows, int K, int E) {
     const Plan p = make_plan(n, E);
     if (p.by_runs) return RunSpace(nullptr, n, p).bytes;
     const size_t table = up(sizeof(uint32_t) << p.bits) + up((sizeof(uint32_t) << p.bits) * p.blocks);
-    // keys and pairs between passes, twice when there are two gaps or more
-    const size_t lists = p.passes > 1 ? 2 * up(sizeof(uint32_t) * (size_t)n) * (p.passes > 2 ? 2 : 1) : 0;
+    // a list between passes, two when there are two gaps or more
+    const size_t lists = p.passes > 1 ? up(sizeof(uint2) * (size_t)n) * (p.passes > 2 ? 2 : 1) : 0;
     return table + lists;
 }
 
@@ -755,23 +752,20 @@ cudaError_t launch_route(const int32_t *ids, long long n_rows, int K, int E, int
     w += up(sizeof(uint32_t) << p.bits);
     uint32_t *counts = reinterpret_cast<uint32_t *>(w);
     w += up((sizeof(uint32_t) << p.bits) * p.blocks);
-    const size_t list = up(sizeof(uint32_t) * (size_t)n);
-    uint32_t *buf[2][2];
-    for (int g = 0; g < 2; ++g)
-        for (int h = 0; h < 2; ++h) buf[g][h] = reinterpret_cast<uint32_t *>(w + (size_t)(2 * g + h) * list);
-    const uint32_t *keys = nullptr, *pairs = nullptr;
+    const size_t list = up(sizeof(uint2) * (size_t)n);
+    const uint2 *items = nullptr;
     for (int q = 0; q < p.passes; ++q) {
         const bool last = q == p.passes - 1;
         const int shift = q * p.bits;
-        count_kernel<<<p.blocks, THREADS, D * sizeof(uint32_t), st>>>(ids, keys, n, E, p.per_block, shift, p.bits,
+        count_kernel<<<p.blocks, THREADS, D * sizeof(uint32_t), st>>>(ids, items, n, E, p.per_block, shift, p.bits,
                                                                       counts, nullptr);
         scan_kernel<<<D, THREADS, 0, st>>>(counts, p.blocks, totals);
-        uint32_t *ko = last ? nullptr : buf[q & 1][0], *po = last ? nullptr : buf[q & 1][1];
-        move_kernel<<<p.blocks, THREADS, move_shared(D), st>>>(
-            ids, keys, pairs, n, E, p.per_block, shift, p.bits, counts, totals, ko, po, last ? order : nullptr,
-            last ? place : nullptr, last && p.passes == 1 ? offsets : nullptr, nullptr);
-        keys = ko;
-        pairs = po;
+        uint2 *to = last ? nullptr : reinterpret_cast<uint2 *>(w + (size_t)(q & 1) * list);
+        move_kernel<<<p.blocks, THREADS, move_shared(D), st>>>(ids, items, n, E, p.per_block, shift, p.bits, counts,
+                                                               totals, to, last ? order : nullptr,
+                                                               last ? place : nullptr,
+                                                               last && p.passes == 1 ? offsets : nullptr, nullptr);
+        items = to;
     }
     if (p.passes > 1) offsets_kernel<<<E / THREADS + 1, THREADS, 0, st>>>(ids, order, n, E, offsets);
     return cudaGetLastError();
