@@ -163,13 +163,14 @@ __global__ void __launch_bounds__(BLOCK ? block_bound(VEC, NV) : THREADS) norm_k
     }
 }
 
-// SUMS: also the block's partial dgamma and dbeta, partial[block][2][D]
+// SUMS: also the block's sums for dgamma and dbeta, 2 D elements from block to
+// block (one block: dgamma and dbeta themselves)
 // BLOCK: 0, or the most threads of a block that shares a row
 template <typename T, int VEC, int NV, int BLOCK, bool SUMS>
 __global__ void __launch_bounds__(BLOCK ? BLOCK : THREADS, BLOCK ? 1 : 2) norm_backward_kernel(
     const T *dy, long long lddy, const T *__restrict__ x, long long ldx, const float *__restrict__ gamma,
     const float *__restrict__ mean, const float *__restrict__ rstd, long long n, int D, int log_l, T *dx,
-    long long lddx, float *__restrict__ partial) {
+    long long lddx, float *__restrict__ sum_g, float *__restrict__ sum_b) {
     __shared__ float scratch[2][2][32];
     const int L = BLOCK ? blockDim.x : 1 << log_l;
     const int lane = threadIdx.x & (BLOCK ? 0xffff : L - 1);
@@ -259,7 +260,8 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : THREADS, BLOCK ? 1 : 2) norm_b
         }
     }
     if (!SUMS) return;
-    float *out = partial + (size_t)blockIdx.x * 2 * D;
+    sum_g += (size_t)blockIdx.x * 2 * D;
+    sum_b += (size_t)blockIdx.x * 2 * D;
     if (BLOCK) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -267,8 +269,8 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : THREADS, BLOCK ? 1 : 2) norm_b
             for (int q = 0; q < VEC; ++q) {
                 const int c = c0 + i * step + q;
                 if (c0 + i * step >= D) break;
-                out[c] = dg[i * VEC + q];
-                out[D + c] = db[i * VEC + q];
+                sum_g[c] = dg[i * VEC + q];
+                sum_b[c] = db[i * VEC + q];
             }
         }
         return;
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(BLOCK ? BLOCK : THREADS, BLOCK ? 1 : 2) norm_b
             float s = 0.0f;
 #pragma unroll
             for (int q = 0; q < THREADS / 32; ++q) s += join[q * D + c];
-            out[which * D + c] = s;
+            (which ? sum_b : sum_g)[c] = s;
         }
     }
 }
@@ -468,7 +470,7 @@ template <typename T, int NV, int ROWS, bool SUMS>
 __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
     const T *dy, long long lddy, const T *__restrict__ x, long long ldx, const float *__restrict__ gamma,
     const float *__restrict__ mean, const float *__restrict__ rstd, long long n, int D, T *dx, long long lddx,
-    float *__restrict__ partial) {
+    float *__restrict__ sum_g, float *__restrict__ sum_b) {
     constexpr int VEC = 16 / sizeof(T);
     using R = Ring<T, NV, ROWS>;
     extern __shared__ uint4 ring_base[];
@@ -603,7 +605,8 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
         }
     }
     if (!SUMS) return;
-    float *out = partial + (size_t)blockIdx.x * 2 * D;
+    sum_g += (size_t)blockIdx.x * 2 * D;
+    sum_b += (size_t)blockIdx.x * 2 * D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * blockDim.x + threadIdx.x;
@@ -611,8 +614,8 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_wide_backward_kernel(
 #pragma unroll
         for (int q = 0; q < VEC; q += 2) {
             const int k = (i * VEC + q) / 2;
-            both(dg[k], out[c * VEC + q], out[c * VEC + q + 1]);
-            both(db[k], out[D + c * VEC + q], out[D + c * VEC + q + 1]);
+            both(dg[k], sum_g[c * VEC + q], sum_g[c * VEC + q + 1]);
+            both(db[k], sum_b[c * VEC + q], sum_b[c * VEC + q + 1]);
         }
     }
 }
@@ -762,38 +765,48 @@ cudaError_t forward(RowsIn x, const float *gamma, const float *beta, float eps, 
 template <typename T> constexpr int lane_elems() { return 32 / sizeof(T); }
 constexpr int BLOCK_ELEMS = 16;
 
+// Where a backward pass puts its blocks' sums: into dgamma and dbeta where
+// there is one block, else into the workspace, for the second kernel
+struct Sums {
+    float *dgamma, *dbeta, *partial;
+    bool wanted() const { return dgamma != nullptr; }
+    float *g(int blocks) const { return blocks == 1 ? dgamma : partial; }
+    float *b(int blocks, int D) const { return blocks == 1 ? dbeta : partial + D; }
+};
+
 // most blocks of a backward pass, a partial row each
 long long backward_blocks(int D) { return D <= 1024 ? SMS * 8 : D <= 4096 ? SMS * 4 : SMS * 2; }
 
 template <typename T, int VEC, int NV, int BLOCK>
 int backward_shape(const Shape &s, RowsIn dy, RowsIn x, const float *gamma, const float *mean, const float *rstd,
-                   long long n, int D, RowsOut dx, float *partial, cudaStream_t st) {
+                   long long n, int D, RowsOut dx, Sums sums, cudaStream_t st) {
     const T *dyp = static_cast<const T *>(dy.p), *xp = static_cast<const T *>(x.p);
-    auto kernel = partial ? norm_backward_kernel<T, VEC, NV, BLOCK, true> : norm_backward_kernel<T, VEC, NV, BLOCK, false>;
-    const size_t shared = partial && !BLOCK ? sizeof(float) * (THREADS / 32) * D : 0;
+    auto kernel = sums.wanted() ? norm_backward_kernel<T, VEC, NV, BLOCK, true> : norm_backward_kernel<T, VEC, NV, BLOCK, false>;
+    const size_t shared = sums.wanted() && !BLOCK ? sizeof(float) * (THREADS / 32) * D : 0;
     static const int registers[2] = {registers_of(norm_backward_kernel<T, VEC, NV, BLOCK, false>),
                                      registers_of(norm_backward_kernel<T, VEC, NV, BLOCK, true>)};
-    const int blocks = resident_blocks(registers[partial != nullptr], s.threads, shared, s.blocks, backward_blocks(D));
+    const int blocks = resident_blocks(registers[sums.wanted()], s.threads, shared, s.blocks, backward_blocks(D));
     kernel<<<blocks, s.threads, shared, st>>>(dyp, dy.ld, xp, x.ld, gamma, mean, rstd, n, D, s.log_l,
-                                              static_cast<T *>(dx.p), dx.ld, partial);
+                                              static_cast<T *>(dx.p), dx.ld, sums.g(blocks), sums.b(blocks, D));
     return blocks;
 }
 
 template <typename T, int NV>
 int backward_wide(RowsIn dy, RowsIn x, const float *gamma, const float *mean, const float *rstd, long long n, int D,
-                  RowsOut dx, float *partial, cudaStream_t st, cudaError_t &e) {
+                  RowsOut dx, Sums sums, cudaStream_t st, cudaError_t &e) {
     const int threads = wide_threads(D * (int)sizeof(T) / 16, NV);
     constexpr int ROWS = wide_rows(NV);
     const size_t shared = Ring<T, NV, ROWS>::bytes(threads);
-    auto kernel = partial ? norm_wide_backward_kernel<T, NV, ROWS, true> : norm_wide_backward_kernel<T, NV, ROWS, false>;
+    auto kernel = sums.wanted() ? norm_wide_backward_kernel<T, NV, ROWS, true> : norm_wide_backward_kernel<T, NV, ROWS, false>;
     e = allow_shared(kernel, shared);
     if (e != cudaSuccess) return 0;
     static const int registers[2] = {registers_of(norm_wide_backward_kernel<T, NV, ROWS, false>),
                                      registers_of(norm_wide_backward_kernel<T, NV, ROWS, true>)};
-    const int blocks = resident_blocks(registers[partial != nullptr], threads, shared, (n + ROWS - 1) / ROWS,
+    const int blocks = resident_blocks(registers[sums.wanted()], threads, shared, (n + ROWS - 1) / ROWS,
                                        backward_blocks(D));
     kernel<<<blocks, threads, shared, st>>>(static_cast<const T *>(dy.p), dy.ld, static_cast<const T *>(x.p), x.ld,
-                                            gamma, mean, rstd, n, D, static_cast<T *>(dx.p), dx.ld, partial);
+                                            gamma, mean, rstd, n, D, static_cast<T *>(dx.p), dx.ld, sums.g(blocks),
+                                            sums.b(blocks, D));
     return blocks;
 }
 
@@ -801,7 +814,7 @@ template <typename T, int VEC>
 cudaError_t backward(RowsIn dy, RowsIn x, const float *gamma, const float *mean, const float *rstd, long long n,
                      int D, RowsOut dx, float *dgamma, float *dbeta, float *partial, cudaStream_t st) {
     const int pieces = (D + VEC - 1) / VEC;
-    float *p = dgamma ? partial : nullptr;
+    const Sums p{dgamma, dbeta, partial};
     constexpr bool WHOLE = VEC * sizeof(T) == 16;
     constexpr int NV = lane_elems<T>() / VEC;
     int blocks = 0;
@@ -821,7 +834,8 @@ cudaError_t backward(RowsIn dy, RowsIn x, const float *gamma, const float *mean,
                                   : backward_shape<T, VEC, M, 1024>(s, dy, x, gamma, mean, rstd, n, D, dx, p, st);
     }
     if (e != cudaSuccess) return e;
-    if (p) norm_join_kernel<<<(2 * D + 31) / 32, JOIN_WARPS * 32, 0, st>>>(p, blocks, D, dgamma, dbeta);
+    if (p.wanted() && blocks > 1)
+        norm_join_kernel<<<(2 * D + 31) / 32, JOIN_WARPS * 32, 0, st>>>(partial, blocks, D, dgamma, dbeta);
     return cudaGetLastError();
 }
 

@@ -39,18 +39,21 @@ def _rows(name: str, x, shape=None, like=None):
         _refuse(f"{name} must be on a CUDA device")
     if like is not None and (x.dtype != like.dtype or x.device != like.device):
         _refuse(f"{name} must have the type and the device of the other rows")
-    if shape is not None and tuple(x.shape) != tuple(shape):
-        _refuse(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
     T, D = x.shape
+    if shape is not None and (T, D) != shape:
+        _refuse(f"{name} has shape {(T, D)}, expected {tuple(shape)}")
     if D < 1:
         _refuse(f"{name} has no columns")
-    if (D > 1 and x.stride(1) != 1) or (T > 1 and x.stride(0) < D):
+    if x.is_contiguous():
+        return D
+    ld, step = x.stride()
+    if (D > 1 and step != 1) or (T > 1 and ld < D):
         _refuse(f"{name}: a row's elements must be consecutive and rows must not overlap")
-    return x.stride(0) if T > 1 else D
+    return ld if T > 1 else D
 
 
-def _dense(name: str, x, dtype, shape, device):
-    if not isinstance(x, torch.Tensor) or x.dtype != dtype or tuple(x.shape) != tuple(shape):
+def _dense(name, x, dtype, shape, device):
+    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape:
         _refuse(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
     if x.device != device or not x.is_contiguous():
         _refuse(f"{name} must be dense and on {device}")
@@ -77,6 +80,11 @@ def _run(device, call, *args):
 
 def _at(x):
     return None if x is None else x.data_ptr()
+
+
+def _float32(x, *shape):
+    """An uninitialised float32 tensor beside x."""
+    return x.new_empty(shape) if x.dtype is torch.float32 else x.new_empty(shape, dtype=torch.float32)
 
 
 # workspace sizes are functions of the sizes alone
@@ -158,7 +166,7 @@ class Route:
         ldx, dw = 0, None
         if x is not None:
             ldx = _rows("x", x, (self.T, D), dxs)
-            dw = x.new_empty((self.T, self.K), dtype=torch.float32)
+            dw = _float32(x, self.T, self.K)
         lddx = D
         if dx is None:
             dx = dxs.new_empty((self.T, D))
@@ -199,7 +207,7 @@ class Route:
         ldy, dw = 0, None
         if y is not None:
             ldy = _rows("y", y, (self.T * self.K, D), dout)
-            dw = y.new_empty((self.T, self.K), dtype=torch.float32)
+            dw = _float32(y, self.T, self.K)
         lddy = D
         if dy is None:
             dy = dout.new_empty((self.T * self.K, D))
@@ -278,7 +286,8 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, out=None):
         out = x.new_empty((T, D))
     else:
         ldy = _rows("out", out, (T, D), x)
-    mean, rstd = x.new_empty(T, dtype=torch.float32), x.new_empty(T, dtype=torch.float32)
+    like = x if gamma is None else gamma
+    mean, rstd = _float32(like, T), _float32(like, T)
     _run(dev, _lib.load().sad_layer_norm, _TYPES[x.dtype], x.data_ptr(), ldx, _at(gamma), _at(beta), eps, T, D,
          out.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr())
     return out, mean, rstd
