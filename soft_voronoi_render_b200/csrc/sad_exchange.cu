@@ -20,10 +20,9 @@
 //
 // Measured (copy rate 6,540 GB/s): 16,384 x 8 rows of 2048 bf16, bound by
 // memory: dispatch 99 us (0.94 of it), combine 87 (1.06), combine's backward
-// 171 (1.02), dispatch's 106 (0.97).  Blend of 2048 x 2048 x 32 bf16 186 us
-// (0.45): every row of F is read for about 256 pixels, 2.1 GB through the L1,
-// which is busy 93 % of the time; its dot products 203 us.  768 x 512 x 64 f16
-// 34 us.
+// 171 (1.02), dispatch's 106 (0.97).  Blend of 2048 x 2048 x 32 bf16 168 us
+// (0.50): every row of F is read for about 256 pixels, 2.1 GB through the L1;
+// its dot products 192 us.  768 x 512 x 64 f16 33 us.
 #include <algorithm>
 
 #include "sad_features.h"
@@ -663,17 +662,19 @@ struct Shape {
 
 // A group loops over its row's pieces.  With fewer lanes a row's ids, weights
 // and dot products are handled fewer times over, with more the loads of a row
-// lie closer: 16-byte pieces, two a lane (2048 x 2048 x 32 bf16: blend 190 us
-// with two lanes, 212 with four; 768 x 512 x 64 f16: 38 with four, 43 with
-// eight, 53 with two); smaller ones, up to eight a lane while a group's load
-// has 16 bytes (768 x 512 x 41 f32: 74 to 86 us, 168 with 32 lanes).  Few rows
-// get all the lanes that a row has pieces for, and wide ones a block.
-Shape shape_of(long long n, int D, int vec, int bytes) {
+// lie closer.  16-byte pieces: gathers up to four a lane, two lanes at the
+// least (1024 x 1024 x 64 f32: 86 us, 104 with two a lane, 147 with one; 2048 x
+// 2048 x 32 bf16: 168 us with two lanes, 192 with one, 212 with four), spreads
+// two (65,536 x 8 of 256 bf16: 51 us, 55 with four); smaller ones, up to eight
+// a lane while a group's load has 16 bytes (768 x 512 x 41 f32: 84 us, 168 with
+// 32 lanes).  Few rows get all the lanes that a row has pieces for, and wide
+// ones a block.
+Shape shape_of(long long n, int D, int vec, int bytes, bool gathers) {
     Shape s;
     s.log_l = group_log(D, vec);
     s.row_per_block = D > 32 * vec && n < 148 * 8;
     const int pieces = (D + vec - 1) / vec;
-    const int fewest = vec * bytes == 16 ? max(1, s.log_l - 1)
+    const int fewest = vec * bytes == 16 ? max(1, s.log_l - (gathers ? 2 : 1))
                                          : min(5, max(ceil_log2(16 / (vec * bytes)), ceil_log2((pieces + 7) / 8)));
     while (!s.row_per_block && pieces <= 256 && s.log_l > fewest && (n << (s.log_l - 1)) / 32 >= 148 * 64) --s.log_l;
     s.turns = 0;  // used with 16-byte pieces
@@ -703,7 +704,7 @@ cudaError_t gather(RowsIn rows, const int32_t *at, long long n_at, const float *
                    int D, RowsOut out, float *dots, cudaStream_t st) {
     const T *r = static_cast<const T *>(rows.p), *g = static_cast<const T *>(other.p);
     T *o = static_cast<T *>(out.p);
-    const Shape s = shape_of(n, D, VEC, sizeof(T));
+    const Shape s = shape_of(n, D, VEC, sizeof(T), true);
     const uint32_t m = (uint32_t)n_at;
     const bool full = K == K_MAX && aligned16(at) && aligned16(w) && aligned16(dots);
     if (o && dots) {
@@ -737,7 +738,7 @@ cudaError_t spread(RowsIn x, const int32_t *at, long long n_at, const float *w, 
                    int D, RowsOut to, float *dots, cudaStream_t st) {
     const T *xp = static_cast<const T *>(x.p), *r = static_cast<const T *>(rows.p);
     T *o = static_cast<T *>(to.p);
-    const Shape s = shape_of(n, D, VEC, sizeof(T));
+    const Shape s = shape_of(n, D, VEC, sizeof(T), false);
     const uint32_t m = (uint32_t)n_at;
     const bool full = K == K_MAX && aligned16(at) && aligned16(w) && aligned16(dots);
     if (dots) {
