@@ -19,10 +19,10 @@
 // then writes its part of order and place, in the pairs' own order.
 //
 // Measured: those lists 454 us (0.14 of the copy rate by the floor's bytes; 196
-// us of it the tiles' sort, bound by instructions and shared memory, 109 us
-// their writing, 90 us the runs' sort); 768 x 512 x 8 pairs of 50,000 sites 89
-// us, 65,536 x 8 of 512 experts 27 us, up to 1024 pairs 3 us in
-// one launch.
+// us of it the tiles' sort, bound by instructions and shared memory, 110 us
+// their writing, 74 us the runs' sort, 51 us the runs' lists, places and
+// offsets); 768 x 512 x 8 pairs of 50,000 sites 89 us, 65,536 x 8 of 512
+// experts 27 us, up to 1024 pairs 3 us in one launch.
 #include "sad_features.h"
 
 namespace sad {
@@ -46,7 +46,7 @@ struct Plan {
 // Tiles that are sorted in shared memory, and the pairs from which on they are:
 // a dozen launches against the scattered writes of seven.  Lists of images:
 // 393,216 x 8 122 us by runs, 95 without; 1,048,576 x 8 206 and 233; 4,194,304
-// x 8 462 and 1,082.  (Random lists of 4,194,304 x 8 over 131,072 sites have no
+// x 8 462 and 1,040.  (Random lists of 4,194,304 x 8 over 131,072 sites have no
 // runs: 3.6 ms against 2.4.)
 constexpr int RUN_ITEMS = 16;
 constexpr int RUN_TILE = THREADS * RUN_ITEMS;
