@@ -619,7 +619,10 @@ int sad_layer_norm_backward(int dtype, const void *dy, int64_t lddy, const void 
  * entries all fail to count, or whose logits are all -infinity has loss 0
  * and gradient 0, whatever else it holds (a teacher class that the student
  * masks with -infinity in a row that keeps others gives an infinite loss and
- * a finite gradient).  dlogits (the type of logits) NULL: loss only; it may
+ * a finite gradient).  The row's maximum is subtracted before anything is
+ * rounded: what a row's logits have in common changes nothing.  (The float32
+ * rounding of the divergence is multiplied by tau^2 as the divergence is.)
+ * dlogits (the type of logits) NULL: loss only; it may
  * be logits (same ld).  1 <= M <= 128, V < 2^30, 1e-30 <= tau <=
  * 1e30. */
 #define SAD_DISTILL_MAX_M 128

@@ -5,7 +5,9 @@
 // With q = softmax(teacher / tau) over the counting entries and p =
 // softmax(z / tau): loss = rw tau^2 sum_m q_m (ln q_m - ln p[id_m]) and dz_v =
 // rw tau (p_v - sum of q_m over id_m = v).  Exponentials are taken to base 2
-// of z log2(e) / tau, about the row's maximum, in float32.
+// of (z - max) log2(e) / tau in float32.  The row's maximum is subtracted before
+// the product is rounded: what all logits have in common leaves no trace, and no
+// tau makes the rounding of z log2(e) / tau count.
 //
 // Bound by memory where rows are read and written once; the exponentials (16
 // a clock on a multiprocessor, two an element with the gradient of a long
@@ -98,21 +100,21 @@ __device__ __forceinline__ float lanes_max(float v, int L) {
 // shared memory.
 struct Teacher {
     int32_t *id;  // -1: does not count
-    float *q;     // first the logit (base 2), then the probability
-    float *zid;   // the student's logit of the class (base 2)
+    float *q;     // first the logit, then the probability
+    float *zid;   // the student's logit of the class
     float max, sum;  // the largest logit, -infinity where no entry counts
 };
 
 template <typename T>
 __device__ __forceinline__ void teacher_load(Teacher &t, const int32_t *__restrict__ tid, const float *__restrict__ tl,
-                                             const T *row, int V, int M, float k, bool in, int lane, int L) {
+                                             const T *row, int V, int M, bool in, int lane, int L) {
     float big = minus_infinity();
     for (int m = lane; m < M; m += L) {
         int32_t id = in ? __ldg(tid + m) : -1;
         float l = minus_infinity(), z = 0.0f;
         if ((uint32_t)id < (uint32_t)V) {
-            l = __ldg(tl + m) * k;
-            z = to_f32<T>(row[id]) * k;
+            l = __ldg(tl + m);
+            z = to_f32<T>(row[id]);
         }
         if (l == minus_infinity()) id = -1;  // a NaN logit of a valid class counts, and shows
         big = max_nan(big, l);
@@ -124,26 +126,26 @@ __device__ __forceinline__ void teacher_load(Teacher &t, const int32_t *__restri
 }
 
 // a lane's share of the sum of exponentials about t.max
-__device__ __forceinline__ float teacher_sum(const Teacher &t, int M, int lane, int L) {
+__device__ __forceinline__ float teacher_sum(const Teacher &t, int M, float k, int lane, int L) {
     float s = 0.0f;
     const float m0 = finite_max(t.max);
-    for (int m = lane; m < M; m += L) s += exp2_fast(t.q[m] - m0);
+    for (int m = lane; m < M; m += L) s += exp2_fast((t.q[m] - m0) * k);
     return s;
 }
 
 // the row's divergence (before rw tau^2), given the student's maximum and sum;
 // leaves q in shared memory
-__device__ __forceinline__ float teacher_loss(Teacher &t, int M, int lane, int L, float big, float sum) {
+__device__ __forceinline__ float teacher_loss(Teacher &t, int M, float k, int lane, int L, float big, float sum) {
     const float is = reciprocal(t.sum), more = log2f(sum * is);
     const float m0 = finite_max(t.max);
     float part = 0.0f;
     for (int m = lane; m < M; m += L) {
         float q = 0.0f;
         if (t.id[m] >= 0) {
-            const float l = t.q[m] - m0;
+            const float l = (t.q[m] - m0) * k;
             q = exp2_fast(l) * is;
             // log q - log p with both maxima taken out first
-            if (q != 0.0f) part = fmaf(q, (l - (t.zid[m] - big)) + more, part);
+            if (q != 0.0f) part = fmaf(q, fmaf(big - t.zid[m], k, l) + more, part);
         }
         t.q[m] = q;
     }
@@ -151,13 +153,14 @@ __device__ __forceinline__ float teacher_loss(Teacher &t, int M, int lane, int L
 }
 
 // gradient of entry m's class, all of its entries counted
-__device__ __forceinline__ float teacher_grad(const Teacher &t, int M, int m, float big, float inv_sum, float scale) {
+__device__ __forceinline__ float teacher_grad(const Teacher &t, int M, float k, int m, float big, float inv_sum,
+                                              float scale) {
     const int32_t id = t.id[m];
     float q = 0.0f;
 #pragma unroll 4
     for (int j = 0; j < M; ++j)
         if (t.id[j] == id) q += t.q[j];
-    return scale * (exp2_fast(t.zid[m] - big) * inv_sum - q);
+    return scale * (exp2_fast((t.zid[m] - big) * k) * inv_sum - q);
 }
 
 // the largest of a piece's elements and m, as loaded; 16-bit ones in pairs
@@ -176,19 +179,19 @@ template <typename T, int VEC> __device__ __forceinline__ float piece_max(const 
     }
 }
 
-// e = 2^(z k - big) of a piece
+// e = 2^((z - big) k) of a piece
 template <typename T, int VEC>
 __device__ __forceinline__ void piece_exp(const Pack<T, VEC> &p, float k, float big, float (&e)[VEC]) {
     if constexpr (VEC % 2 == 0) {
 #pragma unroll
         for (int q = 0; q < VEC; q += 2) {
-            both(fma_two(two(p.get(q), p.get(q + 1)), two(k, k), two(-big, -big)), e[q], e[q + 1]);
+            both(mul_two(add_two(two(p.get(q), p.get(q + 1)), two(-big, -big)), two(k, k)), e[q], e[q + 1]);
             e[q] = exp2_fast(e[q]);
             e[q + 1] = exp2_fast(e[q + 1]);
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) e[q] = exp2_fast(fmaf(p.get(q), k, -big));
+        for (int q = 0; q < VEC; ++q) e[q] = exp2_fast((p.get(q) - big) * k);
     }
 }
 
@@ -278,14 +281,13 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     te.id = reinterpret_cast<int32_t *>(space);
     te.q = space + M;
     te.zid = space + 2 * M;
-    teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, k, in, lane, L);
+    teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, in, lane, L);
 
     float big = EDGES ? edge_z : minus_infinity();
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (lane + i * L < pieces) big = piece_max(p[i], big);
     lanes_max(big, te.max, L);
-    big *= k;
     const bool live = te.max != minus_infinity() && weight != 0.0f && big != minus_infinity();
     if (!live) {  // the row may hold anything: take 0 for it
 #pragma unroll
@@ -305,12 +307,12 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     float sum, other;
     both(sums, sum, other);
     sum += other;
-    const float edge_e = EDGES && edge < V ? exp2_fast(fmaf(edge_z, k, -big)) : 0.0f;
+    const float edge_e = EDGES && edge < V ? exp2_fast((edge_z - big) * k) : 0.0f;
     sum += edge_e;
-    te.sum = teacher_sum(te, M, lane, L);
+    te.sum = teacher_sum(te, M, k, lane, L);
     lanes_sum(sum, te.sum, L);
-    const float part = teacher_loss(te, M, lane, L, big, sum);
-    if (lane == 0 && in) loss[t] = live ? weight * tau * tau * part : 0.0f;
+    const float part = teacher_loss(te, M, k, lane, L, big, sum);
+    if (lane == 0 && in) loss[t] = live ? weight * (tau * (tau * part)) : 0.0f;
     if (!GRAD) return;
     const float scale = weight * tau, is = reciprocal(sum), f = live ? scale * is : 0.0f;
     T *out = dz + t * lddz;
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     // the same value from each of its entries
     if (live)
         for (int m = lane; m < M; m += L)
-            if (te.id[m] >= 0) out[te.id[m]] = from_f32<T>(teacher_grad(te, M, m, big, is, scale));
+            if (te.id[m] >= 0) out[te.id[m]] = from_f32<T>(teacher_grad(te, M, k, m, big, is, scale));
 }
 
 // ---------------------------------------------------------------------------
@@ -360,9 +362,9 @@ __global__ void __launch_bounds__(LONG_THREADS + 32, 4) distill_long_kernel(
 
     Teacher te{s_id, s_q, s_zid, 0.0f, 0.0f};
     if (has_teacher) {
-        teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, k, true, lane, 32);
+        teacher_load<T>(te, tid + t * M, tl + t * M, row, V, M, true, lane, 32);
         te.max = lanes_max(te.max, 32);
-        te.sum = lanes_sum(teacher_sum(te, M, lane, 32), 32);
+        te.sum = lanes_sum(teacher_sum(te, M, k, lane, 32), 32);
         if (lane == 0) t_any = te.max != minus_infinity() ? 1.0f : 0.0f;
     }
 
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(LONG_THREADS + 32, 4) distill_long_kernel(
     float big = minus_infinity(), sum = 0.0f;
     if (edge < V) {
         big = to_f32<T>(row[edge]);
-        sum = big == minus_infinity() ? 0.0f : exp2_fast(fmaf(big, k, -big * k));
+        sum = big == minus_infinity() ? 0.0f : exp2_fast((big - big) * k);  // 1, or NaN
     }
     const float edge_z = big;
     for (int c = first + threadIdx.x; c < last; c += UNROLL * B) {
@@ -390,8 +392,8 @@ __global__ void __launch_bounds__(LONG_THREADS + 32, 4) distill_long_kernel(
             if (GRAD && CACHE && at < last) cache[at - first] = *reinterpret_cast<const uint4 *>(&p[u]);
             m = piece_max(p[u], m);
         }
-        const float m0 = finite_max(m) * k;
-        Two s = two(sum * exp2_fast(big == minus_infinity() ? big : fmaf(big, k, -m0)), 0.0f);
+        const float m0 = finite_max(m);
+        Two s = two(sum * exp2_fast((big - m0) * k), 0.0f);  // exactly sum where the maximum stays
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             if (c + u * B < last) {
@@ -427,21 +429,20 @@ __global__ void __launch_bounds__(LONG_THREADS + 32, 4) distill_long_kernel(
         sum = lanes_sum(wm == minus_infinity() ? 0.0f : ws * exp2_fast((wm - finite_max(big)) * k), 32);
         cluster.sync();  // no block leaves before all have read its shared memory
     }
-    big *= k;
     const bool live = t_any != 0.0f && weight != 0.0f && big != minus_infinity();
     const float scale = weight * tau, is = reciprocal(sum), f = scale * is;
     if (has_teacher) {
-        const float part = teacher_loss(te, M, lane, 32, big, sum);
-        if (lane == 0 && rank == 0) loss[t] = live ? weight * tau * tau * part : 0.0f;
+        const float part = teacher_loss(te, M, k, lane, 32, big, sum);
+        if (lane == 0 && rank == 0) loss[t] = live ? weight * (tau * (tau * part)) : 0.0f;
         if (GRAD) {
             __syncwarp();
-            for (int m = lane; m < M; m += 32) s_zid[m] = teacher_grad(te, M, m, big, is, scale);
+            for (int m = lane; m < M; m += 32) s_zid[m] = teacher_grad(te, M, k, m, big, is, scale);
         }
     }
     if (!GRAD) return;
     T *out = dz + t * lddz, *out_body = out + cut.head;
     const bool whole = same_boundaries(out, row);
-    if (edge < V) out[edge] = from_f32<T>(live ? exp2_fast(fmaf(edge_z, k, -big)) * f : 0.0f);
+    if (edge < V) out[edge] = from_f32<T>(live ? exp2_fast((edge_z - big) * k) * f : 0.0f);
     if (live) {
         for (int c = first + threadIdx.x; c < last; c += UNROLL * B) {
             Pack<T, VEC> p[UNROLL];

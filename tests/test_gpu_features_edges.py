@@ -1,0 +1,148 @@
+"""Feature-field operators where rows share an offset, temperatures are
+extreme, rows are constant, sites outnumber the pairs by far, and a field's
+lists or graphs change between calls.
+
+u = 2^-24 is the most a float32 operation is off by, relative to its result; a
+16-bit result is rounded once more, by half a step.
+"""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def feat():
+    from soft_voronoi_render_b200 import features
+    return features
+
+
+def rng(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def teacher(g, T, V, M):
+    """M distinct classes a row and their logits, one of them empty."""
+    tid = (torch.randint(0, V, (T, 1), generator=g, device="cuda") + torch.arange(M, device="cuda") * (V // M)) % V
+    tid = tid.int().contiguous()
+    if M > 2:
+        tid[:, 1] = -1
+    return tid, randn(g, T, M).mul_(2.0)
+
+
+@pytest.mark.parametrize("dt,step,offset", [("f32", 2.0 ** -8, 1000.0), ("f32", 2.0 ** -8, -30000.0),
+                                            ("f16", 0.25, 500.0), ("bf16", 0.5, -100.0)])
+@pytest.mark.parametrize("T,V,M", [(300, 19, 4), (65, 150, 8), (9, 1001, 16), (7, 5000, 8), (3, 40001, 32),
+                                   (1, 300001, 64)])
+def test_distill_of_rows_that_share_an_offset(T, V, M, dt, step, offset):
+    """A softmax does not see what all logits of a row have in common: logits
+    on a grid that holds both z and z + offset give the same bits, the
+    teacher's too."""
+    f, t = feat(), TYPES[dt]
+    g = rng(V)
+    z = (randn(g, T, V).mul_(2.0 / step).round() * step).clamp(-8.0, 8.0)
+    tid, tl = teacher(g, T, V, M)
+    tl = (tl * 256.0).round() / 256.0
+    for tau in (1.0, 0.3):
+        loss, dz = f.distill(z.to(t), tid, tl, tau)
+        loss2, dz2 = f.distill((z + offset).to(t), tid, tl, tau)
+        loss3, dz3 = f.distill(z.to(t), tid, tl + 1000.0, tau)
+        assert torch.equal(loss, loss2) and torch.equal(dz, dz2)
+        assert torch.equal(loss, loss3) and torch.equal(dz, dz3)
+        assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(dz).all())
+
+
+@pytest.mark.parametrize("offset", [0.0, 1000.0, -20000.0])
+@pytest.mark.parametrize("T,V,M", [(300, 19, 4), (65, 150, 8), (9, 1001, 16), (7, 5000, 8), (3, 40001, 32),
+                                   (1, 300001, 64)])
+def test_distill_error_goes_by_the_distance_from_the_maximum(T, V, M, offset):
+    """Against 64 bits, with a tolerance in which the logits' size has no part.
+
+    An argument (z - max) k takes a subtraction and a product, and k (log2(e)
+    rounded, divided by tau) is off by 2 u: 4 u of its size, d in natural
+    units; the exponential adds 2 ulp, 4 u.  A sum of V exponentials adds its
+    depth, and a running maximum rescales it: by (4 span + 4) u for each
+    change, whose distances add up to the row's span; V / 8192 + 4 at most.
+    """
+    f = feat()
+    g = rng(V + 1)
+    z = randn(g, T, V).mul_(2.0) + offset
+    tid, tl = teacher(g, T, V, M)
+    tl = tl + offset / 4
+    rw = torch.rand(T, generator=g, device="cuda") + 0.5
+    for tau in (1.0, 0.3):
+        loss, dz = f.distill(z, tid, tl, tau, rw)
+        zd, td, w = z.double() / tau, tl.double() / tau, rw.double()
+        ok = tid >= 0
+        at = tid.clamp(min=0).long()
+        td = torch.where(ok, td, -torch.inf)
+        lq, lp = torch.log_softmax(td, 1), torch.log_softmax(zd, 1)
+        q, p = lq.exp(), lp.exp()
+        terms = torch.where(ok, q * (lq - lp.gather(1, at)), 0.0)
+        mass = torch.zeros_like(p).scatter_add_(1, at, torch.where(ok, q, 0.0))
+        rl, rz = w * tau * tau * terms.sum(1), (w * tau)[:, None] * (p - mass)
+        d = zd.max(1, keepdim=True).values - zd
+        span = d.max(1, keepdim=True).values
+        tspan = torch.where(ok, td.max(1, keepdim=True).values - td, 0.0).max(1, keepdim=True).values
+        e_sum = (8 * span + 4 * (V / 8192 + 4) + 4 + min(V + 1, V / 32 + 24)) * U
+        e_q = (8 * tspan + 8 + M) * U
+        size = span + tspan + float(np.log(V) + np.log(M))
+        slack = (w * tau * tau)[:, None] * (e_sum + e_q + size * ((M + 16) * U + e_q))
+        assert bool(((loss.double() - rl).abs() <= slack[:, 0]).all())
+        slack = (w * tau)[:, None] * (p * ((4 * d + 8) * U + e_sum) + mass * (e_q + (M + 4) * U)) + 3 * U * rz.abs()
+        assert bool(((dz.double() - rz).abs() <= slack + 1e-37).all())
+
+
+@pytest.mark.parametrize("V", [20, 150, 1001, 40001, 300001])
+@pytest.mark.parametrize("tau", [1e-30, 1e-12, 1e-6, 1e-3])
+def test_distill_at_sharp_temperatures(V, tau):
+    """Logits at least 1 apart and a small tau: both softmaxes are one class,
+    the loss is tau (max - z of the teacher's class), up to the roundings of
+    its five factors and of k."""
+    f = feat()
+    g = rng(V)
+    T, M = 3, 5
+    z = torch.rand((T, V), generator=g, device="cuda").mul_(50.0)
+    best = torch.randint(0, V - 1, (T,), generator=g, device="cuda")
+    z[torch.arange(T), best] = 60.3
+    tid = ((best[:, None] + 1 + torch.arange(M, device="cuda")) % V).int()
+    tl = torch.tensor([7.7, 3.0, -2.0, 5.1, 0.0], device="cuda").repeat(T, 1)
+    loss, dz = f.distill(z, tid, tl, tau)
+    ref = tau * (z.double().max(1).values - z.gather(1, tid[:, :1].long())[:, 0].double())
+    # (z - max) k, log2 and LN2, tau twice: 16 u covers them
+    assert bool(((loss.double() - ref).abs() <= 16 * U * ref).all()), (loss, ref)
+    want = torch.zeros((T, V), dtype=torch.float64, device="cuda")
+    want[torch.arange(T), best] = tau
+    want[torch.arange(T), tid[:, 0].long()] = -tau
+    assert bool(((dz.double() - want).abs() <= 8 * U * want.abs()).all())
+
+
+def test_distill_at_flat_temperatures():
+    """tau^2 beyond float32: a divergence of 0 stays 0, and the gradient is
+    tau (p - q) as ever."""
+    f = feat()
+    one = torch.zeros((2, 1), device="cuda")
+    loss, dz = f.distill(one, one.int(), one, 1e30)
+    assert loss.tolist() == [0.0, 0.0] and dz.tolist() == [[0.0], [0.0]]
+    z = randn(rng(3), 4, 64)
+    tid, tl = teacher(rng(4), 4, 64, 8)
+    tid[:, 1] = 0
+    _, dz = f.distill(z, tid, tl, 1e20)
+    mass = torch.zeros((4, 64), dtype=torch.float64, device="cuda").scatter_add_(1, tid.long(), torch.full((4, 8), 0.125, device="cuda").double())
+    ref = 1e20 * (1.0 / 64 - mass)
+    # exponentials of 2 ulp, their sum, its reciprocal, the products
+    assert bool(((dz.double() - ref).abs() <= 1e20 * (1.0 / 64 + mass) * 90 * U).all())
