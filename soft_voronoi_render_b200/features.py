@@ -356,8 +356,9 @@ class FeatureField:
     ``features`` (N, D), ``gamma`` and ``beta`` (D) are float32 and the
     caller's to optimise; ``loss_and_grads`` fills ``grad_features``,
     ``grad_gamma`` and ``grad_beta``.  ``update_lists`` takes the current
-    candidate lists; call it after the lists or the sites changed.  The sites
-    themselves are fitted by the colour loss and not moved here.
+    candidate lists; call it after the lists or the sites changed, with their
+    routing before a captured step is replayed.  The sites themselves are
+    fitted by the colour loss and not moved here.
     """
 
     def __init__(self, sad, D: int, seed: int = 1, eps: float = 1e-5):
@@ -373,12 +374,19 @@ class FeatureField:
         self.ids = torch.full((sad.P, 8), -1, dtype=torch.int32, device=sad.device)
         self.weights = torch.zeros((sad.P, 8), **f32)
         self.route = Route(sad.P, 8, sad.N, sad.device)
+        self._routed = True           # by what has run: no lists yet, and no pairs in the route
+        self._unrouted_graph = False  # whether a replay may leave the route behind the lists
 
     def update_lists(self, route: bool = True) -> None:
-        """The lists' ids and weights, and (for fitting) their routing."""
+        """The lists' ids and weights, and (for fitting) their routing; without
+        ``route`` the next ``loss_and_grads`` routes them."""
         self.sad.blend_weights(self.ids, self.weights)
         if route:
             self.route.build(self.ids)
+        if not torch.cuda.is_current_stream_capturing():
+            self._routed = route
+        elif not route:
+            self._unrouted_graph = True
 
     def render(self):
         """The field's (P, D) rows: class logits, or an embedding."""
@@ -387,6 +395,9 @@ class FeatureField:
     def loss_and_grads(self, teacher_ids, teacher_logits, temperature: float = 1.0, row_weight=None):
         """The pixels' distillation losses (P); the D channels are the
         teacher's classes.  Gradients are those of the losses' sum."""
+        if not self._routed or self._unrouted_graph:
+            self.route.build(self.ids)
+            self._routed = self._routed or not torch.cuda.is_current_stream_capturing()
         x = blend(self.features, self.ids, self.weights)
         y, mean, rstd = layer_norm(x, self.gamma, self.beta, self.eps)
         loss, dy = distill(y, teacher_ids, teacher_logits, temperature, row_weight, dlogits=y)

@@ -146,3 +146,65 @@ def test_distill_at_flat_temperatures():
     ref = 1e20 * (1.0 / 64 - mass)
     # exponentials of 2 ulp, their sum, its reciprocal, the products
     assert bool(((dz.double() - ref).abs() <= 1e20 * (1.0 / 64 + mass) * 90 * U).all())
+
+
+def small_field(D=6, seed=2):
+    import synth
+    from soft_voronoi_render_b200 import Sad
+    H, W, N = 24, 40, 60
+    s = Sad(H, W, N, seed=3)
+    s.set_sites(synth.uniform_sites(H, W, N, 4))
+    s.refresh(2)
+    field = feat().FeatureField(s, D, seed=seed)
+    field.features.mul_(100.0)
+    g = rng(9)
+    tid = torch.rand((H * W, D), generator=g, device="cuda").topk(3, 1).indices.int().contiguous()
+    return s, field, tid, randn(g, H * W, 3)
+
+
+def test_gradients_after_lists_were_taken_without_a_route():
+    """update_lists(route=False) leaves the routing to the next gradient,
+    which is that of the lists as they are."""
+    import synth
+    s, field, tid, tl = small_field()
+    field.update_lists(route=False)
+    field.loss_and_grads(tid, tl)
+    first = field.grad_features.clone()
+    field.update_lists()
+    field.loss_and_grads(tid, tl)
+    assert torch.equal(field.grad_features, first) and bool(first.any())
+    s.set_sites(synth.uniform_sites(24, 40, 60, 11))  # other places, other lists
+    s.refresh(2)
+    field.update_lists(route=False)
+    field.loss_and_grads(tid, tl)
+    got = field.grad_features.clone()
+    field.update_lists()
+    field.loss_and_grads(tid, tl)
+    assert torch.equal(got, field.grad_features) and not torch.equal(got, first)
+    # a capture routes too, as often as it is replayed, and says nothing of
+    # what has run
+    s.set_sites(synth.uniform_sites(24, 40, 60, 12))
+    s.refresh(2)
+    field.update_lists(route=False)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        field.loss_and_grads(tid, tl)
+    field.loss_and_grads(tid, tl)
+    eager = field.grad_features.clone()
+    field.grad_features.zero_()
+    graph.replay()
+    assert torch.equal(eager, field.grad_features) and not torch.equal(eager, got)
+    # lists that a graph takes: each of its replays is seen
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        field.update_lists(route=False)
+    for seed in (13, 14):
+        s.set_sites(synth.uniform_sites(24, 40, 60, seed))
+        s.refresh(2)
+        graph.replay()
+        field.loss_and_grads(tid, tl)
+        got = field.grad_features.clone()
+        field.update_lists()
+        field.loss_and_grads(tid, tl)
+        assert torch.equal(got, field.grad_features) and not torch.equal(got, eager)
+    s.close()
