@@ -208,3 +208,45 @@ def test_gradients_after_lists_were_taken_without_a_route():
         field.loss_and_grads(tid, tl)
         assert torch.equal(got, field.grad_features) and not torch.equal(got, eager)
     s.close()
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("D", [3, 19, 33, 64, 250, 516, 1000, 2500, 5000, 5001, 12000, 16384])
+def test_layer_norm_of_constant_rows(D, dt):
+    """Rows of equal elements have that mean, and give beta, whatever bits the
+    element has."""
+    f, t = feat(), TYPES[dt]
+    g = rng(D)
+    c = torch.cat([torch.tensor([0.1, 1000.3, -3.7e-4, 65000.0], device="cuda"), randn(g, 60) * 100.0]).to(t)
+    beta = randn(g, D).to(t).float()
+    for x in (c[:, None].repeat(1, D), torch.cat([c] * 12)[:, None].repeat(1, D)):
+        y, mean, rstd = f.layer_norm(x, None, beta, 1e-5)
+        assert torch.equal(mean, x[:, 0].float())
+        assert torch.equal(y, beta.to(t).expand_as(y))
+        # eps as given, and rsqrtf within 2 ulp
+        assert bool(((rstd.double() * 1e-5 ** 0.5 - 1.0).abs() <= 5 * U).all())
+
+
+@pytest.mark.parametrize("D", [19, 64, 250, 1000, 4096, 5001, 16384])
+def test_layer_norm_mean_goes_by_the_spread(D):
+    """Rows at 1000 +- 0.1.  The mean is corrected by the mean of the
+    deviations from its first value m1: it is off by its own rounding, u |m|,
+    and by the correction's error, depth + 4 roundings of the deviations."""
+    f = feat()
+    x = 1000.0 + 0.1 * randn(rng(D), 700, D)
+    y, mean, rstd = f.layer_norm(x, None, None, 1e-6)
+    xd = x.double()
+    m = xd.mean(1)
+    depth = D + 1 if D < 1024 else D // 32 + 16
+    spread = (xd - m[:, None]).abs().mean(1)
+    first = (depth + 2) * U * xd.abs().mean(1)
+    em = 1.01 * U * m.abs() + (depth + 4) * U * (spread + first)
+    assert bool(((mean.double() - m).abs() <= em).all())
+    var = ((xd - m[:, None]) ** 2).mean(1) + 1e-6
+    rs = var.rsqrt()
+    # the variance about m1, less the square of the correction: depth + 6
+    # roundings of a sum of at most var + first^2
+    ev = (depth + 6) * U * (var + 2 * first ** 2) / (2 * var) + 4 * U
+    assert bool(((rstd.double() / rs - 1.0).abs() <= ev).all())
+    h = (xd - m[:, None]) * rs[:, None]
+    assert bool(((y.double() - h).abs() <= (em * rs)[:, None] + h.abs() * (ev[:, None] + 4 * U)).all())
