@@ -385,13 +385,16 @@ template <int VEC> __device__ __forceinline__ void store_sums(float *to, const f
     }
 }
 
-// the last e in [0, E) with offsets[e] <= s, for s below offsets[E]
-__device__ __forceinline__ int expert_at(const int32_t *__restrict__ offsets, int E, uint32_t s) {
-    int lo = 0, hi = E;  // offsets[lo] <= s < offsets[hi]
+// the last e in [lo, E) with offsets[e] <= s, for offsets[lo] <= s < offsets[E]:
+// by a warp, 32 probes a step.  (Offsets that do not ascend give some e of the
+// range: every step cuts it to a 32nd.)
+__device__ __forceinline__ int expert_at(const int32_t *__restrict__ offsets, int lo, int E, uint32_t s) {
+    int hi = E;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((uint32_t)__ldg(offsets + mid) <= s) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) / 32, at = lo + step * (1 + (int)(threadIdx.x & 31));
+        const bool below = at < hi && (uint32_t)__ldg(offsets + at) <= s;
+        lo += step * __popc(__ballot_sync(0xffffffffu, below));
+        hi = min(hi, lo + step);
     }
     return lo;
 }
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 4) chunk_kernel(const T *__restrict__
     if (lane == 0 && blockIdx.y == 0) cut_expert[chunk] = -1;
     if (lo >= total) return;
     const uint32_t hi = min(lo + C, total);
-    const int first = expert_at(offsets, E, lo);
+    const int first = expert_at(offsets, 0, E, lo);
     constexpr int NP = lane_pieces<T, VEC>();
     const int step = VEC << log_l, wide = NP * step;
     for (int slab = blockIdx.y * wide; slab < D; slab += gridDim.y * wide) {
@@ -421,8 +424,8 @@ __global__ void __launch_bounds__(THREADS, 4) chunk_kernel(const T *__restrict__
         uint32_t a = lo;
         while (a < hi && e < E) {
             const uint32_t end = min((uint32_t)__ldg(offsets + e + 1), total);
-            if (end <= a) {
-                ++e;
+            if (end <= a) {  // no pairs: on to the expert of position a, which may be far
+                e = max(e + 1, expert_at(offsets, e, E, a));
                 continue;
             }
             const uint32_t b = min(end, hi);
