@@ -293,9 +293,10 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, out=None):
     return out, mean, rstd
 
 
-def layer_norm_backward(dy, x, gamma, mean, rstd, want_affine: bool = True, dx=None):
+def layer_norm_backward(dy, x, gamma, mean, rstd, want_affine: bool = True, dx=None, dgamma=None, dbeta=None):
     """(dx, dgamma, dbeta) from the saved mean and rstd; without
-    ``want_affine`` the last two are None.  ``dx`` may be dy."""
+    ``want_affine`` the last two are None.  ``dx`` may be dy; ``dgamma`` and
+    ``dbeta``, dense float32, are given together."""
     ld, ldx = _rows("dy", dy), _rows("x", x, None, dy)
     T, D = x.shape
     dev = x.device
@@ -310,10 +311,15 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, want_affine: bool = True, dx=N
         dx = x.new_empty((T, D))
     else:
         lddx = _rows("dx", dx, (T, D), x)
-    dgamma = dbeta = ws = None
-    nbytes = 0
+    ws, nbytes = None, 0
+    if (dgamma is None) != (dbeta is None) or (dgamma is not None and not want_affine):
+        _refuse("dgamma and dbeta are given together, and wanted")
     if want_affine:
-        dgamma, dbeta = mean.new_empty(D), mean.new_empty(D)
+        if dgamma is None:
+            dgamma, dbeta = mean.new_empty(D), mean.new_empty(D)
+        else:
+            _dense("dgamma", dgamma, torch.float32, (D,), dev)
+            _dense("dbeta", dbeta, torch.float32, (D,), dev)
         nbytes = _norm_bytes(T, D)
         ws = mean.new_empty(-(-nbytes // 4))
     _run(dev, _lib.load().sad_layer_norm_backward, _TYPES[x.dtype], dy.data_ptr(), ld, x.data_ptr(), ldx, _at(gamma),
@@ -355,7 +361,8 @@ class FeatureField:
 
     ``features`` (N, D), ``gamma`` and ``beta`` (D) are float32 and the
     caller's to optimise; ``loss_and_grads`` fills ``grad_features``,
-    ``grad_gamma`` and ``grad_beta``.  ``update_lists`` takes the current
+    ``grad_gamma`` and ``grad_beta``, the same buffers at every call.
+    ``update_lists`` takes the current
     candidate lists; call it after the lists or the sites changed, with their
     routing before a captured step is replayed.  The sites themselves are
     fitted by the colour loss and not moved here.
@@ -370,7 +377,7 @@ class FeatureField:
         self.features = torch.randn((sad.N, self.D), generator=gen, **f32).mul_(0.01)
         self.gamma, self.beta = torch.ones(self.D, **f32), torch.zeros(self.D, **f32)
         self.grad_features = torch.zeros((sad.N, self.D), **f32)
-        self.grad_gamma = self.grad_beta = None
+        self.grad_gamma, self.grad_beta = torch.zeros(self.D, **f32), torch.zeros(self.D, **f32)
         self.ids = torch.full((sad.P, 8), -1, dtype=torch.int32, device=sad.device)
         self.weights = torch.zeros((sad.P, 8), **f32)
         self.route = Route(sad.P, 8, sad.N, sad.device)
@@ -401,6 +408,7 @@ class FeatureField:
         x = blend(self.features, self.ids, self.weights)
         y, mean, rstd = layer_norm(x, self.gamma, self.beta, self.eps)
         loss, dy = distill(y, teacher_ids, teacher_logits, temperature, row_weight, dlogits=y)
-        dx, self.grad_gamma, self.grad_beta = layer_norm_backward(dy, x, self.gamma, mean, rstd, dx=dy)
+        dx, _, _ = layer_norm_backward(dy, x, self.gamma, mean, rstd, dx=dy, dgamma=self.grad_gamma,
+                                       dbeta=self.grad_beta)
         blend_backward(dx, self.features, self.ids, self.weights, self.route, dF=self.grad_features)
         return loss

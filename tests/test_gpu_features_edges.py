@@ -286,3 +286,41 @@ def test_blend_backward_of_few_rows_over_many_sites(T, E, D, dt):
     # ms for 2^21 of them, 20 for 131,072 split over two chunks.  Clearing dF
     # takes up to 0.06 ms.
     assert min(times) < 2.0, times
+
+
+def test_gradients_of_a_field_are_one_set_of_buffers():
+    """Captured steps and eager ones fill the same three buffers: after a
+    replay all of them are the replayed step's."""
+    s, field, tid, tl = small_field()
+    assert field.grad_gamma.shape == field.grad_beta.shape == (field.D,)
+    field.update_lists()
+    other = -tl
+    grads = lambda: [v.clone() for v in (field.grad_features, field.grad_gamma, field.grad_beta)]
+    field.loss_and_grads(tid, tl)
+    want = grads()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        field.loss_and_grads(tid, tl)
+    field.loss_and_grads(tid, other)
+    assert not torch.equal(field.grad_gamma, want[1])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(grads(), want))
+    s.close()
+
+
+def test_layer_norm_backward_into_given_sums():
+    f = feat()
+    from soft_voronoi_render_b200 import SadError
+    for T, D in ((1, 64), (500, 19), (300, 4096), (0, 8)):
+        g = rng(D)
+        x, dy, gamma = randn(g, T, D), randn(g, T, D), randn(g, D)
+        _, mean, rstd = f.layer_norm(x, gamma)
+        _, dg, db = f.layer_norm_backward(dy, x, gamma, mean, rstd)
+        a, b = torch.full((D,), 7.0, device="cuda"), torch.full((D,), 7.0, device="cuda")
+        _, dg2, db2 = f.layer_norm_backward(dy, x, gamma, mean, rstd, dgamma=a, dbeta=b)
+        assert dg2 is a and db2 is b and torch.equal(a, dg) and torch.equal(b, db)
+    for kw in (dict(dgamma=a), dict(dgamma=a, dbeta=b, want_affine=False), dict(dgamma=a[:4], dbeta=b[:4]),
+               dict(dgamma=a.half(), dbeta=b)):
+        with pytest.raises(SadError):
+            f.layer_norm_backward(dy, x, gamma, mean, rstd, **kw)
