@@ -107,9 +107,11 @@ class Route:
     def __init__(self, n_rows: int, K: int, n_sites: int, device="cuda"):
         self.T, self.K, self.E = int(n_rows), int(K), int(n_sites)
         ws = _lib.sad_route_workspace_bytes(self.T, self.K, self.E)
+        device = torch.device(device)
+        if device.type != "cuda":
+            _refuse(f"a route must be on a CUDA device, not on {device}")
         if not torch.cuda.is_available():
             raise SadError(_lib.SAD_ERR_CUDA, "no CUDA device is available")
-        device = torch.device(device)
         i32 = dict(dtype=torch.int32, device=device)
         self.offsets = torch.zeros(self.E + 1, **i32)
         self.order = torch.full((self.T * self.K,), -1, **i32)
