@@ -21,10 +21,12 @@
 // cluster of up to eight blocks that join maxima and sums through distributed
 // shared memory.
 //
-// Measured (copy rate 6,540 GB/s), with the gradient: 393,216 x 150 f32 102 us
+// Measured (copy rate 6,540 GB/s), with the gradient: 393,216 x 150 f32 103 us
 // (0.74 of it; a third of its instructions are the teacher's side of rows of
-// 150), 4096 x 50,001 bf16 170 us (0.74; the part in shared memory, two blocks
-// a multiprocessor, took 205), 1 x 128,000 bf16 7 us.
+// 150), 4096 x 50,001 bf16 172 us (0.73; the part in shared memory, two blocks
+// a multiprocessor, took 205 where this took 172), 1 x 128,000 bf16 7 us;
+// loss only 74, 80 and 6 us.  The teacher's side of a short row goes by M^2:
+// 393,216 x 100 f32 88 us with M = 8, 611 with 32, 1,982 with 64.
 #include <algorithm>
 #include <type_traits>
 

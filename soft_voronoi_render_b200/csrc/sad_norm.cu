@@ -6,8 +6,9 @@
 // spread is small beside its mean (under 1/32 of it) has its mean and variance
 // corrected by the mean of its deviations, which leaves roundings of the
 // spread's size (4096 x 8192 f32 53 us, 51 without; for every row the wide forms
-// took 3 to 7 % longer).  Backward, with g = dy gamma and h = (x - mean) rstd: dx = rstd (g -
-// mean(g) - h mean(g h)), dgamma = sum over rows of dy h, dbeta = sum of dy.
+// took 3 to 7 % longer).
+// Backward, with g = dy gamma and h = (x - mean) rstd: dx = rstd (g - mean(g) - h
+// mean(g h)), dgamma = sum over rows of dy h, dbeta = sum of dy.
 //
 // Bound by memory: x and y once forward; dy, x and dx once backward.
 //
@@ -17,18 +18,19 @@
 // loads and sums fill the first one's waits); backward, as many blocks as
 // stay resident take rows in turn, and every thread copies its own pieces of
 // the rows ahead into shared memory asynchronously (cp.async) and reads back
-// only what it copied, so the copies need no barrier and up to 96 KB a block
-// are on their way.  Rows that no 16-byte piece fits (odd sizes, odd
+// only what it copied, so the copies need no barrier and two steps, up to 128 KB
+// a block, are on their way (none in rows of more than 8192 float32, where one
+// step fills the space).  Rows that no 16-byte piece fits (odd sizes, odd
 // addresses) go in pieces of 4 bytes or one element through registers.
 //
 // Backward, a lane also keeps its columns' dgamma and dbeta in registers; the
 // groups of a block are joined once at its end, and the blocks' partial rows
 // by a second kernel, in a fixed order: a lane adds few rows before the joins
-// (21 for 393,216 rows of 64), which keeps the float32 sums close to their
+// (42 for 393,216 rows of 64), which keeps the float32 sums close to their
 // exact values.
 //
-// Measured (copy rate 6,540 GB/s): 393,216 x 64 f32 forward 31 us (0.99 of
-// it), backward 50 + 3 us (0.87); 8191 x 4096 bf16 forward 27 us (0.77),
+// Measured (copy rate 6,540 GB/s): 393,216 x 64 f32 forward 32 us (0.97 of
+// it), backward 50 + 4 us (0.86); 8191 x 4096 bf16 forward 27 us (0.75),
 // backward 54 + 4 us (0.53, 42 us without dgamma and dbeta): there the sums'
 // registers leave 16 warps a multiprocessor, and what they wait for is one
 // another's reductions (512 threads of half the columns took 81 us).
@@ -350,10 +352,10 @@ __device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.comm
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // One thread's pieces i * blockDim.x + threadIdx.x of ROWS rows of two
-// matrices a step: a ring in shared memory of four steps, the current one
-// among them, or of what 192 KB hold
+// matrices a step: a ring in shared memory of as many steps as 192 KB hold, the
+// current one among them: three, or one of eight pieces
 template <typename T, int NV, int ROWS> struct Ring {
-    static constexpr int VEC = 16 / sizeof(T), FIT = 12 / (NV * ROWS), STAGES = FIT < 4 ? FIT : 4;
+    static constexpr int VEC = 16 / sizeof(T), STAGES = 12 / (NV * ROWS);
     uint4 *base;  // [STAGES][ROWS][2][NV][blockDim.x]
     int slot = 0;
     static size_t bytes(int threads) { return (size_t)STAGES * ROWS * 2 * NV * threads * 16; }

@@ -255,8 +255,8 @@ def test_layer_norm_mean_goes_by_the_spread(D):
 @pytest.mark.parametrize("T,E,D,dt", [(1, 1 << 21, 1, "f32"), (32, 131072, 32, "bf16"), (1000, 131072, 200, "f32"),
                                       (5, 1 << 20, 77, "f16")])
 def test_blend_backward_of_few_rows_over_many_sites(T, E, D, dt):
-    """Sites without pairs cost no more than their zeros: the sums of few rows
-    are right, and clearing dF is most of the time."""
+    """Sites without pairs cost no more than their zeros and a search: the
+    sums of few rows are right, and their time goes by the pairs."""
     f, t = feat(), TYPES[dt]
     g = rng(T)
     ids = torch.randint(0, E, (T, 8), generator=g, device="cuda").int()
