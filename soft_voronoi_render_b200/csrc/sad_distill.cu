@@ -135,23 +135,27 @@ __device__ __forceinline__ float teacher_sum(const Teacher &t, int M, float k, i
     return s;
 }
 
-// the row's divergence (before rw tau^2), given the student's maximum and sum;
-// leaves q in shared memory
-__device__ __forceinline__ float teacher_loss(Teacher &t, int M, float k, int lane, int L, float big, float sum) {
-    const float is = reciprocal(t.sum), more = log2f(sum * is);
+// The row's loss, given scale = rw tau and the student's maximum and sum; leaves
+// q in shared memory.  tau^2 (ln q - ln p) is tau times the logits' distances
+// from their maxima plus tau^2 ln of the sums' quotient: the distances stay
+// unscaled, and half of them is summed, so that a class masked by the lowest
+// float gives a large loss and no infinity.
+__device__ __forceinline__ float teacher_loss(Teacher &t, int M, float k, float tau, float scale, int lane, int L,
+                                              float big, float sum) {
+    const float is = reciprocal(t.sum);
     const float m0 = finite_max(t.max);
     float part = 0.0f;
     for (int m = lane; m < M; m += L) {
         float q = 0.0f;
         if (t.id[m] >= 0) {
-            const float l = (t.q[m] - m0) * k;
-            q = exp2_fast(l) * is;
-            // log q - log p with both maxima taken out first
-            if (q != 0.0f) part = fmaf(q, fmaf(big - t.zid[m], k, l) + more, part);
+            const float l = t.q[m] - m0;
+            q = exp2_fast(l * k) * is;
+            if (q != 0.0f) part = fmaf(0.5f * q, l + (big - t.zid[m]), part);
         }
         t.q[m] = q;
     }
-    return lanes_sum(part, L) * LN2;
+    part = lanes_sum(part, L);
+    return 2.0f * scale * fmaf(0.5f * LN2 * tau, log2f(sum * is), part);
 }
 
 // gradient of entry m's class, all of its entries counted
@@ -313,10 +317,11 @@ __global__ void __launch_bounds__(GROUP_THREADS) distill_group_kernel(
     sum += edge_e;
     te.sum = teacher_sum(te, M, k, lane, L);
     lanes_sum(sum, te.sum, L);
-    const float part = teacher_loss(te, M, k, lane, L, big, sum);
-    if (lane == 0 && in) loss[t] = live ? weight * (tau * (tau * part)) : 0.0f;
+    const float scale = weight * tau;
+    const float part = teacher_loss(te, M, k, tau, scale, lane, L, big, sum);
+    if (lane == 0 && in) loss[t] = live ? part : 0.0f;
     if (!GRAD) return;
-    const float scale = weight * tau, is = reciprocal(sum), f = live ? scale * is : 0.0f;
+    const float is = reciprocal(sum), f = live ? scale * is : 0.0f;
     T *out = dz + t * lddz;
     const bool whole = !EDGES || same_boundaries(out, row);
 #pragma unroll
@@ -434,8 +439,8 @@ __global__ void __launch_bounds__(LONG_THREADS + 32, 4) distill_long_kernel(
     const bool live = t_any != 0.0f && weight != 0.0f && big != minus_infinity();
     const float scale = weight * tau, is = reciprocal(sum), f = scale * is;
     if (has_teacher) {
-        const float part = teacher_loss(te, M, k, lane, 32, big, sum);
-        if (lane == 0 && rank == 0) loss[t] = live ? weight * (tau * (tau * part)) : 0.0f;
+        const float part = teacher_loss(te, M, k, tau, scale, lane, 32, big, sum);
+        if (lane == 0 && rank == 0) loss[t] = live ? part : 0.0f;
         if (GRAD) {
             __syncwarp();
             for (int m = lane; m < M; m += 32) s_zid[m] = teacher_grad(te, M, k, m, big, is, scale);

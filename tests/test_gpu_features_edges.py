@@ -148,6 +148,55 @@ def test_distill_at_flat_temperatures():
     assert bool(((dz.double() - ref).abs() <= 1e20 * (1.0 / 64 + mass) * 90 * U).all())
 
 
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("T,V,M", [(6, 19, 4), (6, 150, 8), (6, 1001, 16), (6, 5000, 8), (6, 40001, 32)])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 2.0])
+def test_distill_of_logits_masked_by_the_lowest_value(T, V, M, dt, tau):
+    """A mask of the type's lowest finite value in place of -infinity: on all
+    of a row, on the teacher's classes too, on all but one class.  The loss
+    then is rw tau q (max - lowest), finite; tolerances as above."""
+    f, t = feat(), TYPES[dt]
+    low = torch.finfo(t).min
+    g = rng(V + M)
+    z = randn(g, T, V).mul_(2.0).to(t)
+    tid = torch.arange(M, device="cuda").int().repeat(T, 1)
+    tl = randn(g, T, M)
+    z[0] = low
+    z[1, :V // 2] = low       # some of the teacher's classes, or all
+    z[2, 1:] = low
+    z[3, M:] = low            # none of them
+    z[4, M - 1] = low
+    rw = torch.tensor([1.0, 0.5, 0.25, 1.0, 0.25, 2.0], device="cuda")
+    loss, dz = f.distill(z, tid, tl, tau, rw)
+    zd, td, w = z.double() / tau, tl.double() / tau, rw.double()
+    lq, lp = torch.log_softmax(td, 1), torch.log_softmax(zd, 1)
+    q, p = lq.exp(), lp.exp()
+    rl = w * tau * tau * (q * (lq - lp.gather(1, tid.long()))).sum(1)
+    mass = torch.zeros_like(p).scatter_add_(1, tid.long(), q)
+    rz = (w * tau)[:, None] * (p - mass)
+    d = zd.max(1, keepdim=True).values - zd
+    span = torch.where(p > 0, d, 0.0).max(1, keepdim=True).values  # beyond it exponentials are 0 on both sides
+    tspan = (td.max(1, keepdim=True).values - td).max(1, keepdim=True).values
+    e_sum = (8 * span + 4 * (V / 8192 + 4) + 4 + min(V + 1, V / 32 + 24)) * U
+    e_q = (8 * tspan + 8 + M) * U
+    far = d.gather(1, tid.long()).max(1, keepdim=True).values
+    size = span + far + tspan + float(np.log(V) + np.log(M))
+    slack = (w * tau * tau)[:, None] * (e_sum + e_q + size * ((M + 16) * U + e_q))
+    # Row 1 with few classes has only masked teacher's classes: at rw tau = 1
+    # (tau 2) its loss is max - lowest, the largest float, and a q above 1 by
+    # its rounding gives infinity: rl + slack > max, so that lies within the
+    # tolerance.  Every other loss has to be finite.
+    fits = rl + slack[:, 0] < torch.finfo(torch.float32).max
+    assert bool(torch.isfinite(loss[fits]).all()) and int((~fits).sum()) <= (tau == 2.0), (loss, rl)
+    assert bool(((loss.double() - rl).abs() <= slack[:, 0])[fits].all())
+    assert bool((loss.double() >= rl - slack[:, 0]).all())
+    half = torch.finfo(t).eps / 2 if t != torch.float32 else 0.0
+    slack = (w * tau)[:, None] * (p * ((4 * torch.where(p > 0, d, 0.0) + 8) * U + e_sum) + mass * (e_q + (M + 4) * U)) \
+        + 3 * U * rz.abs()
+    slack = slack + half * (rz.abs() + slack) + (2.0 ** -25 if t == torch.float16 else 0.0) + 1e-37
+    assert bool(((dz.double() - rz).abs() <= slack).all())
+
+
 def small_field(D=6, seed=2):
     import synth
     from soft_voronoi_render_b200 import Sad
